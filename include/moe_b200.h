@@ -253,6 +253,82 @@ MOE_API moe_status moe_sort_static(const int32_t* idx, int32_t num_tokens, int32
                                    int32_t num_experts, int32_t* perm, int32_t* inv, int32_t* off,
                                    int32_t* status, void* stream);
 
+/* --- ragged products grouped by expert, without a handle ----------------- */
+
+/* Element types of the handle-free operators. */
+typedef enum {
+  MOE_DTYPE_BF16 = 0,
+  MOE_DTYPE_FP16 = 1,
+  MOE_DTYPE_F32 = 2                /* weight gradients only */
+} moe_dtype;
+
+/* Activations fused into a product's epilogue. */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU2 = 1                /* max(v, 0)^2 of the float32 sum; NaN stays NaN */
+} moe_activation;
+
+/* Bounds of the grouped products. */
+#define MOE_GROUPED_MAX_FEATURES 131072
+#define MOE_GROUPED_MAX_ROWS 16777216
+
+/* Products of sorted rows with their experts' matrices (the grouped up and
+ * down projections of MoeLayer `forward_prefill`, on their own), and the two
+ * gradients a training step needs.  K = in_features, N = out_features,
+ * E = num_experts; all tensors are device memory.
+ *
+ *   off [E + 1] int32 (device): expert e owns the rows
+ *     off[e] <= p < off[e + 1], as moe_sort and moe_sort_static write it.
+ *     Groups may be empty.  It is read on the device, at no cost to the host.
+ *   rows: rows of the row tensors (0 <= rows <= MOE_GROUPED_MAX_ROWS).  Rows
+ *     outside every group (below off[0], behind off[E]) are not read as
+ *     operands and not written.
+ *   w [E, N, K], expert e's matrix at element e * N * ldw.
+ *   ld*: elements from one row to the next, at least the row's width.
+ *     Operands (x, dy, w): a multiple of 8; outputs: any.
+ *   dtype: MOE_DTYPE_BF16 or MOE_DTYPE_FP16, of all operands and (except
+ *     out_dtype) of the output.  Sums are float32, rounded once.
+ *   status: optional device int32, OR-ed into (the caller zeroes it): bit 2
+ *     if an entry of off is negative, falls below its predecessor or lies
+ *     beyond `rows` (the group it starts or ends counts as empty, its
+ *     outputs are left as they were), bit 1 if a device-side wait timed out.
+ *   stream: cudaStream_t (NULL = legacy default stream).
+ *
+ * moe_grouped_gemm:        y[p, n]    = act(sum_k x[p, k] w[e(p), n, k])
+ * moe_grouped_gemm_dgrad:  dx[p, k]   = sum_n dy[p, n] w[e(p), n, k]
+ * moe_grouped_gemm_wgrad:  dw[e, n, k] = sum over e's rows of dy[p, n] x[p, k]
+ *   (zero for an empty group); out_dtype is dtype or MOE_DTYPE_F32; with
+ *   accumulate = 1 (MOE_DTYPE_F32 only) the sums are added to dw.
+ *
+ * The calls keep no state and use no workspace: they allocate nothing, may be
+ * captured in a CUDA graph and may overlap in time.  Outputs must not overlap
+ * operands.  The first call of a kind on a device does set-up; make it before
+ * any stream capture.
+ *
+ * Errors (nothing is launched): MOE_ERR_INVALID_CONFIG for num_experts outside
+ * [1, MOE_MAX_EXPERTS], features outside [1, MOE_GROUPED_MAX_FEATURES], a bad
+ * dtype, activation, out_dtype or accumulate, or a leading dimension below
+ * the row's width, above 2^22 - 8 or (operands) no multiple of 8;
+ * MOE_ERR_TOKENS_OUT_OF_RANGE for rows; MOE_ERR_NULL_POINTER;
+ * MOE_ERR_MISALIGNED for an operand off a 16-byte boundary or another pointer
+ * off its element's; MOE_ERR_DEVICE if the current device is not sm_100;
+ * MOE_ERR_CUDA if the launch fails.  With rows = 0 the row tensors may be
+ * NULL (moe_grouped_gemm and moe_grouped_gemm_dgrad then do nothing). */
+MOE_API moe_status moe_grouped_gemm(const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                    const int32_t* off, int32_t num_experts, int32_t rows,
+                                    int32_t in_features, int32_t out_features, int32_t dtype,
+                                    int32_t activation, void* y, int64_t ldy, int32_t* status,
+                                    void* stream);
+MOE_API moe_status moe_grouped_gemm_dgrad(const void* dy, int64_t lddy, const void* w, int64_t ldw,
+                                          const int32_t* off, int32_t num_experts, int32_t rows,
+                                          int32_t in_features, int32_t out_features, int32_t dtype,
+                                          void* dx, int64_t lddx, int32_t* status, void* stream);
+MOE_API moe_status moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                          const int32_t* off, int32_t num_experts, int32_t rows,
+                                          int32_t in_features, int32_t out_features, int32_t dtype,
+                                          void* dw, int64_t lddw, int32_t out_dtype,
+                                          int32_t accumulate, int32_t* status, void* stream);
+
 /* Copy the routing used by the last moe_forward* call on this handle (either
  * path) into idx [T, k] int32 and w [T, k] float32 (device pointers, same
  * meaning as moe_route's outputs); num_tokens must equal that call's. */

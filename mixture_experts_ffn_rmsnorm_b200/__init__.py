@@ -11,7 +11,8 @@ import ctypes
 import os
 from typing import Optional
 
-__all__ = ["load_library", "sort_static", "MoEConfig", "MoELayer", "MoEError", "STATUS",
+__all__ = ["load_library", "sort_static", "grouped_gemm", "grouped_gemm_dgrad",
+           "grouped_gemm_wgrad", "MoEConfig", "MoELayer", "MoEError", "STATUS",
            "PATH_AUTO", "PATH_DECODE", "PATH_PREFILL", "EXPORTED_SYMBOLS", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_b200.so")
@@ -28,7 +29,8 @@ EXPORTED_SYMBOLS = ("moe_create", "moe_forward", "moe_forward_path", "moe_forwar
                     "moe_destroy", "moe_status_string", "moe_route", "moe_sort",
                     "moe_get_device_status", "moe_last_launch_count", "moe_copy_routing",
                     "moe_set_stage_events", "moe_sort_static", "moe_copy_sort",
-                    "moe_last_path")
+                    "moe_last_path", "moe_grouped_gemm", "moe_grouped_gemm_dgrad",
+                    "moe_grouped_gemm_wgrad")
 
 
 class MoEError(RuntimeError):
@@ -72,7 +74,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         from . import build as _build
         _build.build()  # raises when nvcc fails; there is no fallback implementation
     lib = ctypes.CDLL(p)
-    V, I32 = ctypes.c_void_p, ctypes.c_int32
+    V, I32, I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
     sig = {
         "moe_create": ([V, V, V], ctypes.c_int),
         "moe_forward": ([V, V, V, I32, V], ctypes.c_int),
@@ -89,6 +91,12 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "moe_sort_static": ([V, I32, I32, I32, V, V, V, V, V], ctypes.c_int),
         "moe_copy_sort": ([V, V, V, V, I32, V], ctypes.c_int),
         "moe_last_path": ([V], I32),
+        "moe_grouped_gemm": ([V, I64, V, I64, V, I32, I32, I32, I32, I32, I32, V, I64, V, V],
+                             ctypes.c_int),
+        "moe_grouped_gemm_dgrad": ([V, I64, V, I64, V, I32, I32, I32, I32, I32, V, I64, V, V],
+                                   ctypes.c_int),
+        "moe_grouped_gemm_wgrad": ([V, I64, V, I64, V, I32, I32, I32, I32, I32, V, I64, I32, I32,
+                                    V, V], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -118,6 +126,143 @@ def sort_static(idx, top_k, num_experts, perm, inv, off, status=None, stream=Non
                              _ptr(off), _ptr(status), _stream_ptr(stream))
     if st != 0:
         raise MoEError(st, "moe_sort_static")
+
+
+# -- handle-free expert operators ------------------------------------------------
+
+_DTYPES = {}  # torch dtype -> moe_dtype, filled at the first call (torch is imported lazily)
+
+
+def _dtype_code(t, what) -> int:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise MoEError(1, f"{what}: dtype {t.dtype}")
+    return code
+
+
+def _on_device(what, *tensors):
+    """All tensors on the current CUDA device (the library launches there)."""
+    import torch
+    cur = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != cur):
+            raise MoEError(7, f"{what}: a tensor is on {t.device}, not on the current CUDA device")
+
+
+def _rows_ld(t, what, name) -> int:
+    """Leading dimension of a row tensor [rows, width] (unit stride along a row)."""
+    if t.dim() != 2:
+        raise MoEError(1, f"{what}: {name} is not two-dimensional")
+    rows, width = t.shape
+    if width > 1 and rows > 0 and t.stride(1) != 1:
+        raise MoEError(1, f"{what}: {name}'s rows are not contiguous")
+    return t.stride(0) if rows > 1 else (width + 7) // 8 * 8
+
+
+def _experts_ld(t, what, name) -> int:
+    """Leading dimension of stacked matrices [E, N, K]: matrices back to back."""
+    if t.dim() != 3:
+        raise MoEError(1, f"{what}: {name} is not three-dimensional")
+    E, N, K = t.shape
+    if K > 1 and t.stride(2) != 1:
+        raise MoEError(1, f"{what}: {name}'s rows are not contiguous")
+    if N > 1:
+        ld = t.stride(1)
+        if E > 1 and t.stride(0) != N * ld:
+            raise MoEError(1, f"{what}: {name}'s matrices do not lie back to back")
+        return ld
+    return t.stride(0) if E > 1 else (K + 7) // 8 * 8
+
+
+def _check_off(off, E, what):
+    if str(off.dtype) != "torch.int32" or off.dim() != 1 or off.shape[0] != E + 1 or (
+            not off.is_contiguous()):
+        raise MoEError(1, f"{what}: off is not a contiguous int32 tensor [num_experts + 1]")
+
+
+def _check_status(status, what):
+    if status is not None and (str(status.dtype) != "torch.int32" or status.numel() < 1):
+        raise MoEError(1, f"{what}: status is not an int32 tensor")
+
+
+def grouped_gemm(x, w, off, y, relu2=False, status=None, stream=None):
+    """moe_grouped_gemm: y[p] = act(w[e(p)] @ x[p]) for the sorted rows p of
+    each expert e, off[e] <= p < off[e + 1] (as moe_sort writes off).
+
+    x [rows, K], w [E, N, K], y [rows, N], all BF16 or all FP16 (rows may be
+    strided; x's and w's strides are multiples of 8 elements); off [E + 1]
+    int32.  Rows outside every group are left as they are.  relu2 applies
+    max(v, 0)^2.  status: optional int32 word the device ORs error bits into."""
+    what = "moe_grouped_gemm"
+    ldx, ldw, ldy = _rows_ld(x, what, "x"), _experts_ld(w, what, "w"), _rows_ld(y, what, "y")
+    E, N, K = w.shape
+    rows = x.shape[0]
+    if x.shape[1] != K or tuple(y.shape) != (rows, N):
+        raise MoEError(1, f"{what}: shapes {tuple(x.shape)}, {tuple(w.shape)}, {tuple(y.shape)}")
+    dt = _dtype_code(x, what)
+    if w.dtype != x.dtype or y.dtype != x.dtype:
+        raise MoEError(1, f"{what}: x, w and y have different dtypes")
+    _check_off(off, E, what)
+    _check_status(status, what)
+    _on_device(what, x, w, off, y, status)
+    st = load_library().moe_grouped_gemm(_ptr(x), ldx, _ptr(w), ldw, _ptr(off), E, rows, K, N, dt,
+                                         int(relu2), _ptr(y), ldy, _ptr(status),
+                                         _stream_ptr(stream))
+    if st != 0:
+        raise MoEError(st, what)
+
+
+def grouped_gemm_dgrad(dy, w, off, dx, status=None, stream=None):
+    """moe_grouped_gemm_dgrad: dx[p] = w[e(p)]^T @ dy[p], the gradient of
+    grouped_gemm (without its activation) with respect to x.
+
+    dy [rows, N], w [E, N, K], dx [rows, K]; the rest as in grouped_gemm."""
+    what = "moe_grouped_gemm_dgrad"
+    ldy, ldw, ldx = _rows_ld(dy, what, "dy"), _experts_ld(w, what, "w"), _rows_ld(dx, what, "dx")
+    E, N, K = w.shape
+    rows = dy.shape[0]
+    if dy.shape[1] != N or tuple(dx.shape) != (rows, K):
+        raise MoEError(1, f"{what}: shapes {tuple(dy.shape)}, {tuple(w.shape)}, {tuple(dx.shape)}")
+    dt = _dtype_code(dy, what)
+    if w.dtype != dy.dtype or dx.dtype != dy.dtype:
+        raise MoEError(1, f"{what}: dy, w and dx have different dtypes")
+    _check_off(off, E, what)
+    _check_status(status, what)
+    _on_device(what, dy, w, off, dx, status)
+    st = load_library().moe_grouped_gemm_dgrad(_ptr(dy), ldy, _ptr(w), ldw, _ptr(off), E, rows, K,
+                                               N, dt, _ptr(dx), ldx, _ptr(status),
+                                               _stream_ptr(stream))
+    if st != 0:
+        raise MoEError(st, what)
+
+
+def grouped_gemm_wgrad(dy, x, off, dw, accumulate=False, status=None, stream=None):
+    """moe_grouped_gemm_wgrad: dw[e] = sum over e's rows of dy[p] x[p]^T, the
+    gradient of grouped_gemm (without its activation) with respect to w; zero
+    for an empty group.
+
+    dy [rows, N], x [rows, K]; dw [E, N, K] of the same dtype or float32.
+    accumulate (float32 only) adds to dw.  The rest as in grouped_gemm."""
+    what = "moe_grouped_gemm_wgrad"
+    ldy, ldx, ldw = _rows_ld(dy, what, "dy"), _rows_ld(x, what, "x"), _experts_ld(dw, what, "dw")
+    E, N, K = dw.shape
+    rows = dy.shape[0]
+    if dy.shape[1] != N or tuple(x.shape) != (rows, K):
+        raise MoEError(1, f"{what}: shapes {tuple(dy.shape)}, {tuple(x.shape)}, {tuple(dw.shape)}")
+    dt = _dtype_code(dy, what)
+    if x.dtype != dy.dtype:
+        raise MoEError(1, f"{what}: dy and x have different dtypes")
+    _check_off(off, E, what)
+    _check_status(status, what)
+    _on_device(what, dy, x, off, dw, status)
+    st = load_library().moe_grouped_gemm_wgrad(_ptr(dy), ldy, _ptr(x), ldx, _ptr(off), E, rows, K,
+                                               N, dt, _ptr(dw), ldw, _dtype_code(dw, what),
+                                               int(accumulate), _ptr(status), _stream_ptr(stream))
+    if st != 0:
+        raise MoEError(st, what)
 
 
 class MoELayer:

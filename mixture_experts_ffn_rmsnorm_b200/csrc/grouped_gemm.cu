@@ -1,0 +1,692 @@
+// Ragged products grouped by expert on the 5th-generation tensor cores, and
+// their gradients (moe_grouped_gemm, moe_grouped_gemm_dgrad,
+// moe_grouped_gemm_wgrad).
+//
+// Expert e owns rows off[e] <= p < off[e + 1] of the sorted row tensors and
+// the matrix W_e [N, K]:
+//   forward         y[p, n]   = act(sum_k W_e[n, k] x[p, k])
+//   data gradient   dx[p, k]  = sum_n W_e[n, k] dy[p, n]
+//   weight gradient dW_e[n, k] = sum_p dy[p, n] x[p, k]
+// Each is C[r, c] = sum_q A[c, q] B[r, q] per expert, with c the contiguous
+// dimension of the output.  c is the tensor cores' M (TMEM lanes) and r their
+// N (TMEM columns): N comes in steps of 16, so a group of few rows costs a
+// narrow MMA instead of a padded 128-row one, and a warp's lanes hold
+// neighbouring elements of an output row.
+//   forward:         c = n, r = rows, q = k: A = W_e K-major,  B = x K-major
+//   data gradient:   c = k, r = rows, q = n: A = W_e MN-major, B = dy K-major
+//   weight gradient: c = k, r = n, q = rows: A = x MN-major,   B = dy MN-major
+// (a TMA box of 64 contiguous elements x 64 rows lands in shared memory as an
+// MN-major tile as it is; nothing is transposed).
+//
+// Structure: CG CTAs (1, or a cluster of 2) work on one tile of 128 * CG c's
+// x NB r's at a time, persistently, tile indices handed out round-robin over
+// a list that every CTA derives from `off` by itself (no workspace, nothing
+// shared between calls).
+//   warp 0    one lane issues the TMA loads into a ring of stages;
+//   warp 1    one lane (of the pair's rank 0) issues tcgen05.mma;
+//   warp 2    weight gradient: zeroes the rows of a group's last k-block that
+//             belong to the next group, in shared memory;
+//   warps 4-7 read the accumulators from TMEM and store them, while the MMA
+//             warp fills the other accumulator.
+// In a pair each CTA loads its 128 c's of A and half of the r's of B, and
+// reads its half of the accumulator: 64 bytes of shared-memory fill per cycle
+// at the tensor cores' full rate instead of 96 for one CTA with the same NB.
+// Every wait is bounded; a timeout sets a status bit and the CTA winds down.
+#include <cuda_fp16.h>
+
+#include "handle_free.h"
+#include "moe_internal.h"
+#include "ptx_pair.cuh"
+
+namespace moe {
+namespace {
+
+enum Mode : int { kFwd = 0, kDgrad = 1, kWgrad = 2 };
+
+constexpr int kThreads = 256;
+constexpr int kBK = 64;        // elements of q per k-block (128 bytes)
+constexpr int kSmallBox = 16;  // rows of the small K-major box of B
+
+struct GroupedArgs {
+  CUtensorMap tmA;   // forward: 128-row (or kARows) boxes; else 64-row boxes
+  CUtensorMap tmB;   // K-major: NB / CG rows a box; weight gradient: 64
+  CUtensorMap tmBs;  // K-major B in boxes of kSmallBox rows
+  const int* off;
+  int groups;
+  int rows;  // rows of the row tensors: no group may end behind it
+  int C;     // extent of c
+  int Q;     // extent of q (forward, data gradient)
+  int R;     // extent of r (weight gradient)
+  void* out;
+  long long ldo;           // elements
+  long long group_stride;  // elements (weight gradient)
+  uint32_t fmt;            // 0 = FP16, 1 = BF16
+  int relu2;
+  int out_f32;
+  int accumulate;  // out += (FP32 only)
+  int vec;         // 16-byte stores: base, ldo and group_stride allow them
+  int* status;
+};
+
+template <Mode M, int CG, int ROWS_A, int NB, int KPS, int STAGES>
+struct Traits {
+  static constexpr bool kAMN = M != kFwd;
+  static constexpr bool kBMN = M == kWgrad;
+  static constexpr int kABytes = ROWS_A * 128;       // one k-block of A in one CTA
+  static constexpr int kBBytes = NB / CG * 128;      // one k-block of B in one CTA
+  static constexpr int kStageBytes = KPS * (kABytes + kBBytes);
+  static constexpr int kTileC = ROWS_A * CG;
+  static constexpr int kTmemCols = 2 * NB;
+  static constexpr int kStagingBytes = 4 * 32 * 64;
+  static constexpr int kSmem = 1024 + STAGES * kStageBytes + kStagingBytes + 512;
+  static_assert(ROWS_A == 128 || (ROWS_A == 64 && CG == 1), "");
+  // an M = 128 MMA reads 128 rows of A: with 64 loaded rows the others lie in
+  // the B block behind them (their accumulator rows are not stored)
+  static_assert(ROWS_A == 128 || kBBytes >= 64 * 128, "");
+  static_assert(!kBMN || KPS == 1, "the tail of a group is one k-block of one stage");
+  static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols <= 512, "");
+  static_assert(kSmem <= 232448 - 8192, "");  // beside the static tables
+};
+
+struct GTile {
+  int e;
+  int row0;  // forward, data gradient: first row; weight gradient: first q row
+  int cnt;   // rows of the group
+  int r0;    // first r of the tile, inside the group
+  int nr;    // r's of the tile
+  int c0;    // first c of the tile
+  int nk;    // k-blocks
+};
+
+// Tile w of the launch.  `e` is a cursor: the calls of one thread come with
+// increasing w.  pre[e] = tiles of the groups before e.
+template <Mode M, int TILE_C, int NB>
+__device__ __forceinline__ GTile tile_of(const GroupedArgs& p, const int* off, const int* pre,
+                                         int w, int& e) {
+  while (pre[e + 1] <= w) ++e;
+  GTile t;
+  const int ct = (p.C + TILE_C - 1) / TILE_C;
+  const int i = w - pre[e];
+  const int ri = i / ct;
+  t.e = e;
+  t.row0 = off[2 * e];
+  t.cnt = off[2 * e + 1];
+  t.c0 = (i - ri * ct) * TILE_C;
+  t.r0 = ri * NB;
+  const int ext = M == kWgrad ? p.R : t.cnt;
+  t.nr = min(NB, ext - t.r0);
+  t.nk = ((M == kWgrad ? t.cnt : p.Q) + kBK - 1) / kBK;
+  return t;
+}
+
+__device__ __forceinline__ void give_up(const GroupedArgs& p, volatile int* abort) {
+  *abort = 1;
+  if (p.status) atomicOr(p.status, kStatusWaitTimeout);
+}
+
+__device__ __forceinline__ uint16_t to_16(float v, uint32_t fmt) {
+  return fmt ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+
+// 32 accumulator columns (r = j) of this lane's c, to the output.  c is this
+// lane's column, cw the warp's first; n rows are valid.
+__device__ __forceinline__ void store_chunk(const GroupedArgs& p, const uint32_t (&acc)[32],
+                                            uint8_t* staging, long long base, int c, int cw, int n,
+                                            bool cvalid) {
+  const int lane = threadIdx.x & 31;
+  float v[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    v[j] = __uint_as_float(acc[j]);
+    if (p.relu2) v[j] = v[j] <= 0.f ? 0.f : v[j] * v[j];  // NaN stays NaN
+  }
+  if (p.out_f32) {
+    // a lane's neighbours hold the neighbouring c: 128 bytes a row and warp
+    float* o = static_cast<float*>(p.out) + base + c;
+    if (cvalid) {
+      if (p.accumulate) {
+        float old[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) old[j] = j < n ? o[j * p.ldo] : 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += old[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < n) o[j * p.ldo] = v[j];
+    }
+    return;
+  }
+  uint16_t* o = static_cast<uint16_t*>(p.out) + base;
+  if (p.vec && cw + 32 <= p.C) {
+    uint16_t* s = reinterpret_cast<uint16_t*>(staging);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) s[j * 32 + lane] = to_16(v[j], p.fmt);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = i * 8 + (lane >> 2);
+      const uint4 u = *reinterpret_cast<const uint4*>(s + j * 32 + (lane & 3) * 8);
+      if (j < n) *reinterpret_cast<uint4*>(o + j * p.ldo + cw + (lane & 3) * 8) = u;
+    }
+    __syncwarp();
+  } else if (cvalid) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < n) o[j * p.ldo + c] = to_16(v[j], p.fmt);
+  }
+}
+
+template <Mode M, int CG, int ROWS_A, int NB, int KPS, int STAGES>
+__global__ void __launch_bounds__(kThreads, 1)
+    ragged_gemm_kernel(const __grid_constant__ GroupedArgs p) {
+  using Tr = Traits<M, CG, ROWS_A, NB, KPS, STAGES>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t* tiles = smem_raw + pad;
+  uint8_t* staging = tiles + STAGES * Tr::kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + Tr::kStagingBytes);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tail = empty + STAGES;
+  uint64_t* tfull = tail + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((3 * STAGES + 5) * 8 + 8 <= 512, "");
+  __shared__ int s_pre[MOE_MAX_EXPERTS + 1];
+  __shared__ int s_scan[kThreads];
+  __shared__ int s_rows[2 * MOE_MAX_EXPERTS];  // {first row, rows} of each group
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], CG);
+      mbar_init(&empty[s], 1);
+      mbar_init(&tail[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 4 * CG);
+    }
+    mbar_init(drain, 1);
+    *abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&p.tmA);
+    tma_prefetch_desc(&p.tmB);
+  }
+  if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, Tr::kTmemCols);
+
+  // the tile list: tiles of each group, prefix sums
+  {
+    const int ct = (p.C + Tr::kTileC - 1) / Tr::kTileC;
+    const int e = threadIdx.x;
+    int n = 0;
+    if (e < p.groups) {
+      const int a = p.off[e], b = p.off[e + 1];
+      const bool good = a >= 0 && a <= b && b <= p.rows;
+      if (!good && p.status && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
+      const int cnt = good ? b - a : 0;
+      s_rows[2 * e] = good ? a : 0;
+      s_rows[2 * e + 1] = cnt;
+      n = ((M == kWgrad ? p.R : cnt) + NB - 1) / NB * ct;
+      if (M == kWgrad && cnt == 0 && p.accumulate) n = 0;  // nothing to add
+      if (M == kWgrad && !good) n = 0;  // a bad group's gradient is left as it was
+    }
+    s_scan[e] = n;
+    __syncthreads();
+    for (int d = 1; d < kThreads; d *= 2) {
+      const int add = e >= d ? s_scan[e - d] : 0;
+      __syncthreads();
+      s_scan[e] += add;
+      __syncthreads();
+    }
+    if (e == 0) s_pre[0] = 0;
+    if (e < p.groups) s_pre[e + 1] = s_scan[e];
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int W = s_pre[p.groups];
+  const int step = int(gridDim.x) / CG;
+  const int first = int(blockIdx.x) / CG;
+  const uint32_t tiles_u32 = smem_u32(tiles);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int stage = 0, e = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int w = first; w < W && ok; w += step) {
+        const GTile t = tile_of<M, Tr::kTileC, NB>(p, s_rows, s_pre, w, e);
+        const int nmma = (t.nr + 15) & ~15;
+        const int nb = nmma / CG;  // r's of B this CTA loads
+        const int ca = t.c0 + int(rank) * ROWS_A;
+        const int rb = t.r0 + int(rank) * nb;
+        int nbox;  // boxes of B per k-block
+        uint32_t bbytes;
+        if (Tr::kBMN) {
+          nbox = (nb + 63) / 64;
+          bbytes = nbox * 64 * 128;
+        } else {
+          nbox = (nb + kSmallBox - 1) / kSmallBox;
+          if (nbox * 2 > NB / CG / kSmallBox) nbox = 0;  // one large box
+          bbytes = nbox ? nbox * kSmallBox * 128 : Tr::kBBytes;
+        }
+        for (int kb0 = 0; kb0 < t.nk; kb0 += KPS) {
+          if (!mbar_wait_cluster(&empty[stage], phase ^ 1u, abort)) {
+            give_up(p, abort);
+            ok = false;
+            break;
+          }
+          const int kbn = min(KPS, t.nk - kb0);
+          const uint32_t bytes = uint32_t(kbn) * (Tr::kABytes + bbytes);
+          const bool is_tail = M == kWgrad && kb0 + 1 == t.nk && (t.cnt & (kBK - 1)) != 0;
+          uint32_t bar;
+          if (is_tail) {
+            mbar_arrive_expect_tx(&tail[stage], bytes);
+            bar = smem_u32(&tail[stage]);
+          } else if (CG == 2) {
+            bar = map_to_rank(smem_u32(&full[stage]), 0);
+            mbar_arrive_expect_tx_at(bar, bytes);
+          } else {
+            mbar_arrive_expect_tx(&full[stage], bytes);
+            bar = smem_u32(&full[stage]);
+          }
+          for (int kk = 0; kk < kbn; ++kk) {
+            const int kb = kb0 + kk;
+            const uint32_t sa = tiles_u32 + stage * Tr::kStageBytes + kk * (Tr::kABytes + Tr::kBBytes);
+            const uint32_t sb = sa + Tr::kABytes;
+            if constexpr (M == kFwd) {
+              tma_load_3d<CG>(sa, &p.tmA, bar, kb * kBK, ca, t.e);
+            } else {
+              const int y = M == kDgrad ? kb * kBK : t.row0 + kb * kBK;
+              const int z = M == kDgrad ? t.e : 0;
+#pragma unroll
+              for (int h = 0; h < ROWS_A / 64; ++h)
+                tma_load_3d<CG>(sa + h * 8192, &p.tmA, bar, ca + h * 64, y, z);
+            }
+            if constexpr (M == kWgrad) {
+              for (int h = 0; h < nbox; ++h)
+                tma_load_3d<CG>(sb + h * 8192, &p.tmB, bar, rb + h * 64, t.row0 + kb * kBK, 0);
+            } else if (nbox == 0) {
+              tma_load_3d<CG>(sb, &p.tmB, bar, kb * kBK, t.row0 + rb, 0);
+            } else {
+              for (int h = 0; h < nbox; ++h)
+                tma_load_3d<CG>(sb + h * kSmallBox * 128, &p.tmBs, bar, kb * kBK,
+                                t.row0 + rb + h * kSmallBox, 0);
+            }
+          }
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {  // let the copies in flight land before the CTA may exit
+        const long long t0 = clock64();
+        while (clock64() - t0 < 4000000) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0 && rank == 0) {
+      int stage = 0, e = 0, it = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int w = first; w < W && ok; w += step) {
+        const GTile t = tile_of<M, Tr::kTileC, NB>(p, s_rows, s_pre, w, e);
+        if (t.nk == 0) continue;
+        const int nmma = (t.nr + 15) & ~15;
+        const uint32_t idesc = make_idesc_16(128 * CG, nmma, p.fmt, Tr::kAMN, Tr::kBMN);
+        const int ab = it & 1;
+        if (!mbar_wait_cluster(&tempty[ab], ((it >> 1) & 1) ^ 1u, abort)) {
+          give_up(p, abort);
+          break;
+        }
+        ++it;
+        tc_fence_after();
+        const uint32_t d = tmem_base + uint32_t(ab * NB);
+        for (int kb0 = 0; kb0 < t.nk; kb0 += KPS) {
+          if (!mbar_wait_cluster(&full[stage], phase, abort)) {
+            give_up(p, abort);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int kbn = min(KPS, t.nk - kb0);
+          for (int kk = 0; kk < kbn; ++kk) {
+            const uint32_t sa = tiles_u32 + stage * Tr::kStageBytes + kk * (Tr::kABytes + Tr::kBBytes);
+            const uint32_t sb = sa + Tr::kABytes;
+            const uint64_t ad = Tr::kAMN ? smem_desc_mn_sw128(sa, 8192)
+                                         : smem_desc_sw128(tiles + (sa - tiles_u32));
+            const uint64_t bd = Tr::kBMN ? smem_desc_mn_sw128(sb, 8192)
+                                         : smem_desc_sw128(tiles + (sb - tiles_u32));
+            int ks = kBK / 16;
+            if (M == kWgrad && kb0 + kk + 1 == t.nk)
+              ks = (t.cnt - (t.nk - 1) * kBK + 15) / 16;  // only the steps with rows
+#pragma unroll
+            for (int s = 0; s < kBK / 16; ++s)
+              if (s < ks)
+                umma_f16_cg<CG>(d, ad + s * (Tr::kAMN ? 128 : 2), bd + s * (Tr::kBMN ? 128 : 2),
+                                idesc, (kb0 | kk | s) ? 1u : 0u);
+          }
+          umma_commit_cg<CG>(&empty[stage]);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok) umma_commit_cg<CG>(&tfull[ab]);
+      }
+      // every MMA issued has completed once `drain` flips (in both CTAs)
+      umma_commit_cg<CG>(drain);
+      int zero = 0;
+      mbar_wait(drain, 0, &zero);
+    }
+  } else if (M == kWgrad && warp == 2) {
+    // ---------------------------------------- rows behind a group's last one
+    int e = 0, total = 0;
+    uint32_t used = 0;  // phase bit of each stage's tail barrier
+    for (int w = first; w < W; w += step) {
+      const GTile t = tile_of<M, Tr::kTileC, NB>(p, s_rows, s_pre, w, e);
+      total += t.nk;
+      const int valid = t.cnt & (kBK - 1);
+      if (valid == 0) continue;
+      const int stage = (total - 1) % STAGES;
+      if (!mbar_wait(&tail[stage], (used >> stage) & 1u, abort)) {
+        give_up(p, abort);
+        break;
+      }
+      used ^= 1u << stage;
+      const int nb = ((t.nr + 15) & ~15) / CG;
+      const int blocks = ROWS_A / 64 + (nb + 63) / 64;
+      const int end = (valid + 15) & ~15;
+      for (int h = 0; h < blocks; ++h) {
+        uint32_t* blk = reinterpret_cast<uint32_t*>(tiles + stage * Tr::kStageBytes + h * 8192);
+        for (int r = valid; r < end; ++r) blk[r * 32 + lane] = 0u;  // whole rows: swizzled or not
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2)
+          mbar_arrive_at(map_to_rank(smem_u32(&full[stage]), 0));
+        else
+          mbar_arrive(&full[stage]);
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;  // TMEM lane quarter this warp may access
+    uint8_t* st = staging + q * 2048;
+    int e = 0, it = 0;
+    for (int w = first; w < W; w += step) {
+      const GTile t = tile_of<M, Tr::kTileC, NB>(p, s_rows, s_pre, w, e);
+      const int cw = t.c0 + int(rank) * ROWS_A + q * 32;
+      const int c = cw + lane;
+      const bool cvalid = q * 32 < ROWS_A && c < p.C;
+      const long long row = M == kWgrad ? t.r0 : (long long)(t.row0) + t.r0;
+      const long long base = (M == kWgrad ? t.e * p.group_stride : 0) + row * p.ldo;
+      const int ab = it & 1;
+      if (t.nk > 0) {
+        if (!mbar_wait_cluster(&tfull[ab], (it >> 1) & 1, abort)) {
+          give_up(p, abort);
+          break;
+        }
+        ++it;
+        tc_fence_after();
+      }
+      const uint32_t tb = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(ab * NB);
+#pragma unroll 1
+      for (int j0 = 0; j0 < t.nr; j0 += 32) {
+        uint32_t r[32];
+        if (t.nk > 0) {
+          tmem_ld_32x32b_x32(tb + uint32_t(j0), r);
+          tmem_ld_wait();
+        } else {  // an empty group's gradient
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = 0u;
+        }
+        if (q * 32 < ROWS_A && cw < p.C)
+          store_chunk(p, r, st, base + j0 * p.ldo, c, cw, t.nr - j0, cvalid);
+      }
+      if (t.nk > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2)
+            mbar_arrive_at(map_to_rank(smem_u32(&tempty[ab]), 0));
+          else
+            mbar_arrive(&tempty[ab]);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  if constexpr (CG == 2) cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_cg<CG>(tmem_base, Tr::kTmemCols);
+  }
+  if constexpr (CG == 2) {
+    __syncwarp();
+    cluster_sync();
+  }
+}
+
+template <Mode M, int CG, int ROWS_A, int NB, int KPS, int STAGES>
+struct Variant {
+  using Tr = Traits<M, CG, ROWS_A, NB, KPS, STAGES>;
+
+  static cudaError_t launch(const GroupedArgs& a, int dev, int sms, long long max_tiles,
+                            cudaStream_t stream) {
+    // the shared memory limit, once per device
+    static std::atomic<bool> ready[kMaxDevices];
+    auto* fn = ragged_gemm_kernel<M, CG, ROWS_A, NB, KPS, STAGES>;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Tr::kSmem);
+      if (e != cudaSuccess) return e;
+      ready[dev].store(true, std::memory_order_release);
+    }
+    const int units = sms / CG;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(CG * (max_tiles < units ? max_tiles : units)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Tr::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fn, a);
+  }
+
+  // Tiles of `groups` groups with `rows` rows in all, at most.
+  static long long tiles_of(const GroupedArgs& a) {
+    const long long ct = (a.C + Tr::kTileC - 1) / Tr::kTileC;
+    if (M == kWgrad) return a.groups * ct * ((a.R + NB - 1) / NB);
+    return ct * (a.rows / NB + (a.groups < a.rows ? a.groups : a.rows));
+  }
+};
+
+struct Operand {
+  const void* base;
+  long long ld;  // elements
+  int inner, rows, groups;
+};
+
+bool map_of(CUtensorMap* m, const Operand& o, uint32_t fmt, int box_rows) {
+  return make_map_3d(m, fmt ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                     o.base, uint64_t(o.inner), uint64_t(o.rows), uint64_t(o.groups),
+                     uint64_t(o.ld) * 2, uint64_t(o.ld) * 2 * uint64_t(o.groups > 1 ? o.rows : 1),
+                     uint32_t(box_rows));
+}
+
+template <Mode M, int CG, int ROWS_A, int NB, int KPS, int STAGES>
+moe_status run_variant(GroupedArgs& a, const Operand& A, const Operand& B, int dev, int sms,
+                       cudaStream_t stream) {
+  using V = Variant<M, CG, ROWS_A, NB, KPS, STAGES>;
+  bool ok = map_of(&a.tmA, A, a.fmt, M == kFwd ? ROWS_A : 64);
+  ok = ok && map_of(&a.tmB, B, a.fmt, M == kWgrad ? 64 : NB / CG);
+  if (M != kWgrad) ok = ok && map_of(&a.tmBs, B, a.fmt, kSmallBox);
+  if (!ok) return MOE_ERR_CUDA;
+  if (V::launch(a, dev, sms, V::tiles_of(a), stream) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
+// Rules every operand keeps: a leading dimension that covers the row, in
+// 16-byte steps (a TMA stride), and a 16-byte aligned base.
+moe_status check_sizes(int num_experts, int rows, int K, int N, int dtype) {
+  if (num_experts < 1 || num_experts > MOE_MAX_EXPERTS) return MOE_ERR_INVALID_CONFIG;
+  if (K < 1 || K > MOE_GROUPED_MAX_FEATURES || N < 1 || N > MOE_GROUPED_MAX_FEATURES)
+    return MOE_ERR_INVALID_CONFIG;
+  if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_FP16) return MOE_ERR_INVALID_CONFIG;
+  if (rows < 0 || rows > MOE_GROUPED_MAX_ROWS) return MOE_ERR_TOKENS_OUT_OF_RANGE;
+  return MOE_OK;
+}
+
+constexpr int64_t kMaxLd = (int64_t(1) << 22) - 8;  // a group's stride stays below TMA's 2^40 bytes
+
+bool bad_ld(int64_t ld, int width, bool tma) {
+  return ld < width || ld > kMaxLd || (tma && (ld & 7));
+}
+
+template <Mode M>
+moe_status dispatch(GroupedArgs& a, const Operand& A, const Operand& B, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  const moe_status st = current_device(&dev, &sms);
+  if (st != MOE_OK) return st;
+  if constexpr (M != kWgrad) {
+    if (a.rows <= 32LL * a.groups)
+      return run_variant<M, 1, 64, 64, 4, 3>(a, A, B, dev, sms, stream);
+  }
+  return run_variant<M, 2, 128, 256, 1, 6>(a, A, B, dev, sms, stream);
+}
+
+}  // namespace
+}  // namespace moe
+
+using moe::aligned_to;
+
+extern "C" moe_status moe_grouped_gemm(const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                       const int32_t* off, int32_t num_experts, int32_t rows,
+                                       int32_t in_features, int32_t out_features, int32_t dtype,
+                                       int32_t activation, void* y, int64_t ldy, int32_t* status,
+                                       void* stream) {
+  const moe_status st = moe::check_sizes(num_experts, rows, in_features, out_features, dtype);
+  if (st != MOE_OK) return st;
+  if (activation != MOE_ACT_NONE && activation != MOE_ACT_RELU2) return MOE_ERR_INVALID_CONFIG;
+  if (moe::bad_ld(ldx, in_features, true) || moe::bad_ld(ldw, in_features, true) ||
+      moe::bad_ld(ldy, out_features, false))
+    return MOE_ERR_INVALID_CONFIG;
+  if (rows == 0) return MOE_OK;
+  if (!x || !w || !off || !y) return MOE_ERR_NULL_POINTER;
+  if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(y, 2) || !aligned_to(off, 4) ||
+      !aligned_to(status, 4))
+    return MOE_ERR_MISALIGNED;
+  moe::GroupedArgs a = {};
+  a.off = off;
+  a.groups = num_experts;
+  a.rows = rows;
+  a.C = out_features;
+  a.Q = in_features;
+  a.out = y;
+  a.ldo = ldy;
+  a.fmt = dtype == MOE_DTYPE_BF16;
+  a.relu2 = activation == MOE_ACT_RELU2;
+  a.vec = aligned_to(y, 16) && (ldy & 7) == 0;
+  a.status = status;
+  return moe::dispatch<moe::kFwd>(a, {w, ldw, in_features, out_features, num_experts},
+                                  {x, ldx, in_features, rows, 1},
+                                  static_cast<cudaStream_t>(stream));
+}
+
+extern "C" moe_status moe_grouped_gemm_dgrad(const void* dy, int64_t lddy, const void* w,
+                                             int64_t ldw, const int32_t* off, int32_t num_experts,
+                                             int32_t rows, int32_t in_features,
+                                             int32_t out_features, int32_t dtype, void* dx,
+                                             int64_t lddx, int32_t* status, void* stream) {
+  const moe_status st = moe::check_sizes(num_experts, rows, in_features, out_features, dtype);
+  if (st != MOE_OK) return st;
+  if (moe::bad_ld(lddy, out_features, true) || moe::bad_ld(ldw, in_features, true) ||
+      moe::bad_ld(lddx, in_features, false))
+    return MOE_ERR_INVALID_CONFIG;
+  if (rows == 0) return MOE_OK;
+  if (!dy || !w || !off || !dx) return MOE_ERR_NULL_POINTER;
+  if (!aligned_to(dy, 16) || !aligned_to(w, 16) || !aligned_to(dx, 2) || !aligned_to(off, 4) ||
+      !aligned_to(status, 4))
+    return MOE_ERR_MISALIGNED;
+  moe::GroupedArgs a = {};
+  a.off = off;
+  a.groups = num_experts;
+  a.rows = rows;
+  a.C = in_features;
+  a.Q = out_features;
+  a.out = dx;
+  a.ldo = lddx;
+  a.fmt = dtype == MOE_DTYPE_BF16;
+  a.vec = aligned_to(dx, 16) && (lddx & 7) == 0;
+  a.status = status;
+  return moe::dispatch<moe::kDgrad>(a, {w, ldw, in_features, out_features, num_experts},
+                                    {dy, lddy, out_features, rows, 1},
+                                    static_cast<cudaStream_t>(stream));
+}
+
+extern "C" moe_status moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const void* x,
+                                             int64_t ldx, const int32_t* off, int32_t num_experts,
+                                             int32_t rows, int32_t in_features,
+                                             int32_t out_features, int32_t dtype, void* dw,
+                                             int64_t lddw, int32_t out_dtype, int32_t accumulate,
+                                             int32_t* status, void* stream) {
+  const moe_status st = moe::check_sizes(num_experts, rows, in_features, out_features, dtype);
+  if (st != MOE_OK) return st;
+  if (out_dtype != dtype && out_dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_CONFIG;
+  if (accumulate != 0 && (accumulate != 1 || out_dtype != MOE_DTYPE_F32))
+    return MOE_ERR_INVALID_CONFIG;
+  if (moe::bad_ld(lddy, out_features, true) || moe::bad_ld(ldx, in_features, true) ||
+      moe::bad_ld(lddw, in_features, false))
+    return MOE_ERR_INVALID_CONFIG;
+  if (!off || !dw || (rows > 0 && (!dy || !x))) return MOE_ERR_NULL_POINTER;
+  const bool f32 = out_dtype == MOE_DTYPE_F32;
+  if ((rows > 0 && (!aligned_to(dy, 16) || !aligned_to(x, 16))) || !aligned_to(dw, f32 ? 4 : 2) ||
+      !aligned_to(off, 4) || !aligned_to(status, 4))
+    return MOE_ERR_MISALIGNED;
+  moe::GroupedArgs a = {};
+  a.off = off;
+  a.groups = num_experts;
+  a.rows = rows;
+  a.C = in_features;
+  a.R = out_features;
+  a.out = dw;
+  a.ldo = lddw;
+  a.group_stride = (long long)(out_features)*lddw;
+  a.fmt = dtype == MOE_DTYPE_BF16;
+  a.out_f32 = f32;
+  a.accumulate = accumulate;
+  a.vec = !f32 && aligned_to(dw, 16) && (lddw & 7) == 0;
+  a.status = status;
+  // no rows: every group is empty and no map is read through; the maps still
+  // want a valid, aligned address
+  static char none[16] __attribute__((aligned(16)));
+  if (rows == 0) dy = x = none;
+  const int r = rows > 0 ? rows : 1;
+  return moe::dispatch<moe::kWgrad>(a, {x, ldx, in_features, r, 1}, {dy, lddy, out_features, r, 1},
+                                    static_cast<cudaStream_t>(stream));
+}

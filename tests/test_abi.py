@@ -141,3 +141,45 @@ def test_missing_library_fails_loudly():
                        text=True, timeout=120)
     assert r.returncode == 0, r.stderr
     assert r.stdout.startswith("raised"), r.stdout
+
+
+def test_grouped_gemm_validates_on_host():
+    # every rejection happens before the device is touched; 256 stands for any pointer
+    lib = moe.load_library()
+    p = 256
+
+    def fwd(x=p, ldx=64, w=p, ldw=64, off=p, E=4, rows=8, K=64, N=48, dt=0, act=0, y=p, ldy=48):
+        return lib.moe_grouped_gemm(x, ldx, w, ldw, off, E, rows, K, N, dt, act, y, ldy, None, None)
+
+    def dgrad(dy=p, lddy=48, w=p, ldw=64, off=p, E=4, rows=8, K=64, N=48, dt=0, dx=p, lddx=64):
+        return lib.moe_grouped_gemm_dgrad(dy, lddy, w, ldw, off, E, rows, K, N, dt, dx, lddx, None,
+                                          None)
+
+    def wgrad(dy=p, lddy=48, x=p, ldx=64, off=p, E=4, rows=8, K=64, N=48, dt=0, dw=p, lddw=64,
+              odt=0, acc=0):
+        return lib.moe_grouped_gemm_wgrad(dy, lddy, x, ldx, off, E, rows, K, N, dt, dw, lddw, odt,
+                                          acc, None, None)
+
+    for f, ptrs, lds in ((fwd, ("x", "w", "off", "y"), ("ldx", "ldw", "ldy")),
+                         (dgrad, ("dy", "w", "off", "dx"), ("lddy", "ldw", "lddx")),
+                         (wgrad, ("dy", "x", "off", "dw"), ("lddy", "ldx", "lddw"))):
+        for name in ptrs:
+            assert f(**{name: None}) == 2, name
+            assert f(**{name: 257}) == 3, name
+        for name in lds:
+            assert f(**{name: 40}) == 1, name           # narrower than the row
+            assert f(**{name: 1 << 22}) == 1, name
+        for name in lds[:2]:
+            assert f(**{name: 68}) == 1, name           # an operand's stride off 16 bytes
+        for bad in (dict(E=0), dict(E=257), dict(K=0), dict(N=0), dict(K=-1), dict(N=131073),
+                    dict(dt=2), dict(dt=-1)):
+            assert f(**bad) == 1, bad
+        assert f(rows=-1) == 4
+        assert f(rows=16777217) == 4
+    assert fwd(act=2) == 1
+    assert wgrad(odt=1) == 1          # neither the operands' type nor float32
+    assert wgrad(acc=1) == 1          # accumulation wants float32
+    assert wgrad(odt=2, acc=2) == 1
+    assert wgrad(odt=2, dw=258) == 3  # float32 elements
+    assert fwd(rows=0, x=None, y=None) == 0   # nothing to do
+    assert dgrad(rows=0, dy=None, dx=None) == 0
