@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           bbytes = nbox ? nbox * kSmallBox * 128 : Tr::kBBytes;
         }
         for (int kb0 = 0; kb0 < t.nk; kb0 += KPS) {
-          if (!mbar_wait_cluster(&empty[stage], phase ^ 1u, abort)) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort)) {
             give_up(p, abort);
             ok = false;
             break;
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nmma = (t.nr + 15) & ~15;
         const uint32_t idesc = make_idesc_16(128 * CG, nmma, p.fmt, Tr::kAMN, Tr::kBMN);
         const int ab = it & 1;
-        if (!mbar_wait_cluster(&tempty[ab], ((it >> 1) & 1) ^ 1u, abort)) {
+        if (!mbar_wait(&tempty[ab], ((it >> 1) & 1) ^ 1u, abort)) {
           give_up(p, abort);
           break;
         }
@@ -355,7 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t d = tmem_base + uint32_t(ab * NB);
         for (int kb0 = 0; kb0 < t.nk; kb0 += KPS) {
-          if (!mbar_wait_cluster(&full[stage], phase, abort)) {
+          // a group's last k-block: the pair's warps 2 may have written to it
+          const bool is_tail = M == kWgrad && kb0 + 1 == t.nk && (t.cnt & (kBK - 1)) != 0;
+          if (!(CG == 2 && is_tail ? mbar_wait_acquire_cluster(&full[stage], phase, abort)
+                                   : mbar_wait(&full[stage], phase, abort))) {
             give_up(p, abort);
             ok = false;
             break;
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         if (CG == 2)
-          mbar_arrive_at(map_to_rank(smem_u32(&full[stage]), 0));
+          mbar_arrive_release_at(map_to_rank(smem_u32(&full[stage]), 0));
         else
           mbar_arrive(&full[stage]);
       }
@@ -436,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long base = (M == kWgrad ? t.e * p.group_stride : 0) + row * p.ldo;
       const int ab = it & 1;
       if (t.nk > 0) {
-        if (!mbar_wait_cluster(&tfull[ab], (it >> 1) & 1, abort)) {
+        if (!mbar_wait(&tfull[ab], (it >> 1) & 1, abort)) {
           give_up(p, abort);
           break;
         }

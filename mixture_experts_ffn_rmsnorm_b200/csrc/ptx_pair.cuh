@@ -26,40 +26,33 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   return r;
 }
 
+// Arrive on a barrier of the cluster.  Plain: publishes no memory of this
+// thread to other CTAs (barriers that only order async copies, tensor-core
+// work and TMEM reads); a cluster-wide release costs a memory fence of
+// about a microsecond on each call.
 __device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// The same, publishing this thread's earlier shared-memory writes.
+__device__ __forceinline__ void mbar_arrive_release_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive_expect_tx_at(uint32_t cluster_addr, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
-                   cluster_addr),
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
                "r"(bytes)
                : "memory");
 }
 
-// mbar_wait of ptx.cuh for a barrier that another CTA of the cluster arrives on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
-                                                  volatile int* abort) {
-  const uint32_t a = smem_u32(bar);
-  long long t0 = 0;
-  for (bool first = true;; first = false) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(a), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if (first) {
-      t0 = clock64();
-    } else {
-      if (*abort) return false;
-      if (clock64() - t0 > kWaitLimitCycles) return false;
-    }
-  }
+// mbar_wait of ptx.cuh that also acquires what other CTAs of the cluster
+// released on the barrier (mbar_arrive_release_at).
+__device__ __forceinline__ bool mbar_wait_acquire_cluster(uint64_t* bar, uint32_t parity,
+                                                          volatile int* abort) {
+  if (!mbar_wait(bar, parity, abort)) return false;
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  return true;
 }
 
 // 3-D tiled load of one box into this CTA's shared memory.  CG = 2: the
