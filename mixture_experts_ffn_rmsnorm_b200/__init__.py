@@ -130,26 +130,38 @@ def sort_static(idx, top_k, num_experts, perm, inv, off, status=None, stream=Non
 
 # -- handle-free expert operators ------------------------------------------------
 
-_DTYPES = {}  # torch dtype -> moe_dtype, filled at the first call (torch is imported lazily)
+_torch = None
+_DTYPES = {}  # torch dtype -> moe_dtype
+
+
+def _need_torch():
+    """torch, imported at the first call (the binding itself does without)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+        _torch = torch
+    return _torch
 
 
 def _dtype_code(t, what) -> int:
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise MoEError(1, f"{what}: dtype {t.dtype}")
     return code
 
 
-def _on_device(what, *tensors):
-    """All tensors on the current CUDA device (the library launches there)."""
-    import torch
-    cur = torch.cuda.current_device() if torch.cuda.is_available() else -1
+def _launch_stream(what, stream, *tensors) -> Optional[int]:
+    """The stream to launch on; all tensors lie on the current CUDA device,
+    where the library launches."""
+    s = _torch.cuda.current_stream() if stream is None else stream
+    cur = s.device
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != cur):
-            raise MoEError(7, f"{what}: a tensor is on {t.device}, not on the current CUDA device")
+        if t is not None and t.device != cur:
+            raise MoEError(7, f"{what}: a tensor is on {t.device}, not on {cur}")
+    if stream is not None and cur.index != _torch.cuda.current_device():
+        raise MoEError(7, f"{what}: the stream is on {cur}, which is not the current device")
+    return s.cuda_stream or None
 
 
 def _rows_ld(t, what, name) -> int:
@@ -178,13 +190,13 @@ def _experts_ld(t, what, name) -> int:
 
 
 def _check_off(off, E, what):
-    if str(off.dtype) != "torch.int32" or off.dim() != 1 or off.shape[0] != E + 1 or (
+    if off.dtype != _torch.int32 or off.dim() != 1 or off.shape[0] != E + 1 or (
             not off.is_contiguous()):
         raise MoEError(1, f"{what}: off is not a contiguous int32 tensor [num_experts + 1]")
 
 
 def _check_status(status, what):
-    if status is not None and (str(status.dtype) != "torch.int32" or status.numel() < 1):
+    if status is not None and (status.dtype != _torch.int32 or status.numel() < 1):
         raise MoEError(1, f"{what}: status is not an int32 tensor")
 
 
@@ -197,6 +209,7 @@ def grouped_gemm(x, w, off, y, relu2=False, status=None, stream=None):
     int32.  Rows outside every group are left as they are.  relu2 applies
     max(v, 0)^2.  status: optional int32 word the device ORs error bits into."""
     what = "moe_grouped_gemm"
+    _need_torch()
     ldx, ldw, ldy = _rows_ld(x, what, "x"), _experts_ld(w, what, "w"), _rows_ld(y, what, "y")
     E, N, K = w.shape
     rows = x.shape[0]
@@ -207,10 +220,9 @@ def grouped_gemm(x, w, off, y, relu2=False, status=None, stream=None):
         raise MoEError(1, f"{what}: x, w and y have different dtypes")
     _check_off(off, E, what)
     _check_status(status, what)
-    _on_device(what, x, w, off, y, status)
+    s = _launch_stream(what, stream, x, w, off, y, status)
     st = load_library().moe_grouped_gemm(_ptr(x), ldx, _ptr(w), ldw, _ptr(off), E, rows, K, N, dt,
-                                         int(relu2), _ptr(y), ldy, _ptr(status),
-                                         _stream_ptr(stream))
+                                         int(relu2), _ptr(y), ldy, _ptr(status), s)
     if st != 0:
         raise MoEError(st, what)
 
@@ -221,6 +233,7 @@ def grouped_gemm_dgrad(dy, w, off, dx, status=None, stream=None):
 
     dy [rows, N], w [E, N, K], dx [rows, K]; the rest as in grouped_gemm."""
     what = "moe_grouped_gemm_dgrad"
+    _need_torch()
     ldy, ldw, ldx = _rows_ld(dy, what, "dy"), _experts_ld(w, what, "w"), _rows_ld(dx, what, "dx")
     E, N, K = w.shape
     rows = dy.shape[0]
@@ -231,10 +244,9 @@ def grouped_gemm_dgrad(dy, w, off, dx, status=None, stream=None):
         raise MoEError(1, f"{what}: dy, w and dx have different dtypes")
     _check_off(off, E, what)
     _check_status(status, what)
-    _on_device(what, dy, w, off, dx, status)
+    s = _launch_stream(what, stream, dy, w, off, dx, status)
     st = load_library().moe_grouped_gemm_dgrad(_ptr(dy), ldy, _ptr(w), ldw, _ptr(off), E, rows, K,
-                                               N, dt, _ptr(dx), ldx, _ptr(status),
-                                               _stream_ptr(stream))
+                                               N, dt, _ptr(dx), ldx, _ptr(status), s)
     if st != 0:
         raise MoEError(st, what)
 
@@ -247,6 +259,7 @@ def grouped_gemm_wgrad(dy, x, off, dw, accumulate=False, status=None, stream=Non
     dy [rows, N], x [rows, K]; dw [E, N, K] of the same dtype or float32.
     accumulate (float32 only) adds to dw.  The rest as in grouped_gemm."""
     what = "moe_grouped_gemm_wgrad"
+    _need_torch()
     ldy, ldx, ldw = _rows_ld(dy, what, "dy"), _rows_ld(x, what, "x"), _experts_ld(dw, what, "dw")
     E, N, K = dw.shape
     rows = dy.shape[0]
@@ -257,10 +270,10 @@ def grouped_gemm_wgrad(dy, x, off, dw, accumulate=False, status=None, stream=Non
         raise MoEError(1, f"{what}: dy and x have different dtypes")
     _check_off(off, E, what)
     _check_status(status, what)
-    _on_device(what, dy, x, off, dw, status)
+    s = _launch_stream(what, stream, dy, x, off, dw, status)
     st = load_library().moe_grouped_gemm_wgrad(_ptr(dy), ldy, _ptr(x), ldx, _ptr(off), E, rows, K,
                                                N, dt, _ptr(dw), ldw, _dtype_code(dw, what),
-                                               int(accumulate), _ptr(status), _stream_ptr(stream))
+                                               int(accumulate), _ptr(status), s)
     if st != 0:
         raise MoEError(st, what)
 

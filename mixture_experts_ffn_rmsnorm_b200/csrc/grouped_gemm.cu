@@ -26,7 +26,7 @@
 //   warp 1    one lane (of the pair's rank 0) issues tcgen05.mma;
 //   warp 2    weight gradient: zeroes the rows of a group's last k-block that
 //             belong to the next group, in shared memory;
-//   warps 4-7 read the accumulators from TMEM and store them, while the MMA
+//   warps 4-11 read the accumulators from TMEM and store them, while the MMA
 //             warp fills the other accumulator.
 // In a pair each CTA loads its 128 c's of A and half of the r's of B, and
 // reads its half of the accumulator: 64 bytes of shared-memory fill per cycle
@@ -43,7 +43,9 @@ namespace {
 
 enum Mode : int { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+static_assert(kThreads >= MOE_MAX_EXPERTS, "one thread per group derives the tile list");
 constexpr int kBK = 64;        // elements of q per k-block (128 bytes)
 constexpr int kSmallBox = 16;  // rows of the small K-major box of B
 
@@ -51,6 +53,7 @@ struct GroupedArgs {
   CUtensorMap tmA;   // forward: 128-row (or kARows) boxes; else 64-row boxes
   CUtensorMap tmB;   // K-major: NB / CG rows a box; weight gradient: 64
   CUtensorMap tmBs;  // K-major B in boxes of kSmallBox rows
+  CUtensorMap tmO;   // weight gradient with `tma_out`: 32 x 32 boxes of the output
   const int* off;
   int groups;
   int rows;  // rows of the row tensors: no group may end behind it
@@ -62,13 +65,13 @@ struct GroupedArgs {
   long long group_stride;  // elements (weight gradient)
   uint32_t fmt;            // 0 = FP16, 1 = BF16
   int relu2;
-  int out_f32;
   int accumulate;  // out += (FP32 only)
+  int tma_out;     // weight gradient: whole chunks leave by TMA
   int vec;         // 16-byte stores: base, ldo and group_stride allow them
   int* status;
 };
 
-template <Mode M, int CG, int ROWS_A, int NB, int KPS, int STAGES>
+template <Mode M, int CG, int ROWS_A, int NB, int KPS, int STAGES, int EB>
 struct Traits {
   static constexpr bool kAMN = M != kFwd;
   static constexpr bool kBMN = M == kWgrad;
@@ -77,7 +80,8 @@ struct Traits {
   static constexpr int kStageBytes = KPS * (kABytes + kBBytes);
   static constexpr int kTileC = ROWS_A * CG;
   static constexpr int kTmemCols = 2 * NB;
-  static constexpr int kStagingBytes = 4 * 32 * 64;
+  static constexpr int kWarpStaging = 32 * 32 * EB;  // one chunk of the epilogue
+  static constexpr int kStagingBytes = kEpiWarps * kWarpStaging;
   static constexpr int kSmem = 1024 + STAGES * kStageBytes + kStagingBytes + 512;
   static_assert(ROWS_A == 128 || (ROWS_A == 64 && CG == 1), "");
   // an M = 128 MMA reads 128 rows of A: with 64 loaded rows the others lie in
@@ -124,63 +128,123 @@ __device__ __forceinline__ void give_up(const GroupedArgs& p, volatile int* abor
   if (p.status) atomicOr(p.status, kStatusWaitTimeout);
 }
 
-__device__ __forceinline__ uint16_t to_16(float v, uint32_t fmt) {
-  return fmt ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+__device__ __forceinline__ float relu2(float v) {
+  return v <= 0.f ? 0.f : v * v;  // NaN stays NaN
 }
 
-// 32 accumulator columns (r = j) of this lane's c, to the output.  c is this
-// lane's column, cw the warp's first; n rows are valid.
-__device__ __forceinline__ void store_chunk(const GroupedArgs& p, const uint32_t (&acc)[32],
-                                            uint8_t* staging, long long base, int c, int cw, int n,
-                                            bool cvalid) {
-  const int lane = threadIdx.x & 31;
-  float v[32];
-#pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    v[j] = __uint_as_float(acc[j]);
-    if (p.relu2) v[j] = v[j] <= 0.f ? 0.f : v[j] * v[j];  // NaN stays NaN
+__device__ __forceinline__ uint32_t pack_16(uint32_t lo, uint32_t hi, bool bf16) {
+  const float a = __uint_as_float(lo), b = __uint_as_float(hi);
+  if (bf16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
-  if (p.out_f32) {
-    // a lane's neighbours hold the neighbouring c: 128 bytes a row and warp
-    float* o = static_cast<float*>(p.out) + base + c;
-    if (cvalid) {
-      if (p.accumulate) {
-        float old[32];
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Byte offset of the 16-byte block (8 c's) `b` of row r in a warp's 32 x 32
+// staging tile of 16-bit elements: 64 bytes a row, blocks permuted so that
+// neither stmatrix (8 rows of one block) nor the row-wise reads conflict.
+__device__ __forceinline__ uint32_t staging_at(uint32_t r, uint32_t b) {
+  return r * 64 + ((b ^ ((r >> 1) & 3)) * 16);
+}
+
+// A chunk of 32 r's (TMEM columns) x 32 c's (this warp's TMEM lanes), to an
+// output of 16-bit elements.  The accumulators come as fragments of 8 x 8
+// matrices (c x r); two neighbouring r's are rounded into one register, and a
+// transposing stmatrix leaves rows of 32 c's in shared memory, which go out
+// as 16-byte stores.  Measured against one 2-byte store per element and
+// lane into the staging tile: wgrad at 48 rows a group 655 -> see below.
+__device__ __forceinline__ void stage_chunk_16(const GroupedArgs& p, uint32_t (&acc)[2][16],
+                                               uint32_t staging) {
+  const uint32_t lane = threadIdx.x & 31;
+  if (p.relu2) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) old[j] = j < n ? o[j * p.ldo] : 0.f;
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] += old[j];
-      }
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < n) o[j * p.ldo] = v[j];
-    }
-    return;
+      for (int j = 0; j < 16; ++j)
+        acc[h][j] = __float_as_uint(relu2(__uint_as_float(acc[h][j])));
   }
-  uint16_t* o = static_cast<uint16_t*>(p.out) + base;
+  uint32_t m[2][8];
+  if (p.fmt) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m[h][j] = pack_16(acc[h][2 * j], acc[h][2 * j + 1], true);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m[h][j] = pack_16(acc[h][2 * j], acc[h][2 * j + 1], false);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    stmatrix_x4_trans(staging + staging_at(8 * i + (lane & 7), lane >> 3), m[0][2 * i],
+                      m[0][2 * i + 1], m[1][2 * i], m[1][2 * i + 1]);
+}
+
+// A staged chunk to the output, its first n rows.
+__device__ __forceinline__ void store_chunk_16(const GroupedArgs& p, uint32_t staging, uint16_t* o,
+                                               int cw, int n) {
+  const uint32_t lane = threadIdx.x & 31;
   if (p.vec && cw + 32 <= p.C) {
-    uint16_t* s = reinterpret_cast<uint16_t*>(staging);
-#pragma unroll
-    for (int j = 0; j < 32; ++j) s[j * 32 + lane] = to_16(v[j], p.fmt);
-    __syncwarp();
+    const uint32_t b = lane & 3;
+    uint16_t* dst = o + (long long)(lane >> 2) * p.ldo + cw + b * 8;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int j = i * 8 + (lane >> 2);
-      const uint4 u = *reinterpret_cast<const uint4*>(s + j * 32 + (lane & 3) * 8);
-      if (j < n) *reinterpret_cast<uint4*>(o + j * p.ldo + cw + (lane & 3) * 8) = u;
+      const uint32_t r = 8 * i + (lane >> 2);
+      uint4 u;
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                   : "r"(staging + staging_at(r, b)));
+      if (int(r) < n) *reinterpret_cast<uint4*>(dst + 8LL * i * p.ldo) = u;
     }
-    __syncwarp();
-  } else if (cvalid) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < n) o[j * p.ldo + c] = to_16(v[j], p.fmt);
+  } else {
+    const bool cvalid = cw + int(lane) < p.C;
+#pragma unroll 4
+    for (int r = 0; r < 32; ++r) {
+      uint16_t u;
+      asm volatile("ld.shared.u16 %0, [%1];"
+                   : "=h"(u)
+                   : "r"(staging + staging_at(r, lane >> 3) + (lane & 7) * 2));
+      if (r < n && cvalid) o[(long long)r * p.ldo + cw + lane] = u;
+    }
   }
 }
 
-template <Mode M, int CG, int ROWS_A, int NB, int KPS, int STAGES>
+// An FP32 chunk (lane = c): staged as 128-byte rows with the 16-byte blocks
+// permuted as the TMA store's 128-byte swizzle has them.
+__device__ __forceinline__ void stage_chunk_32(const uint32_t (&acc)[32], uint32_t staging) {
+  const uint32_t lane = threadIdx.x & 31;
+#pragma unroll
+  for (uint32_t r = 0; r < 32; ++r)
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(staging + r * 128 +
+                                                 (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4),
+                 "r"(acc[r])
+                 : "memory");
+}
+
+// The same without staging: a warp's store of one r is 128 contiguous bytes.
+__device__ __forceinline__ void store_chunk_32(const GroupedArgs& p, const uint32_t (&acc)[32],
+                                               float* o, int n) {
+  if (p.accumulate) {
+    float old[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) old[j] = j < n ? o[j * p.ldo] : 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < n) o[j * p.ldo] = old[j] + __uint_as_float(acc[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < n) o[j * p.ldo] = __uint_as_float(acc[j]);
+  }
+}
+
+template <Mode M, int CG, int ROWS_A, int NB, int KPS, int STAGES, int EB>
 __global__ void __launch_bounds__(kThreads, 1)
     ragged_gemm_kernel(const __grid_constant__ GroupedArgs p) {
-  using Tr = Traits<M, CG, ROWS_A, NB, KPS, STAGES>;
+  using Tr = Traits<M, CG, ROWS_A, NB, KPS, STAGES, EB>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* tiles = smem_raw + pad;
@@ -195,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   static_assert((3 * STAGES + 5) * 8 + 8 <= 512, "");
   __shared__ int s_pre[MOE_MAX_EXPERTS + 1];
-  __shared__ int s_scan[kThreads];
+  __shared__ int s_scan[kThreads / 32];
   __shared__ int s_rows[2 * MOE_MAX_EXPERTS];  // {first row, rows} of each group
 
   const int warp = threadIdx.x >> 5;
@@ -210,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 4 * CG);
+      mbar_init(&tempty[b], kEpiWarps * CG);
     }
     mbar_init(drain, 1);
     *abort = 0;
@@ -236,16 +300,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (M == kWgrad && cnt == 0 && p.accumulate) n = 0;  // nothing to add
       if (M == kWgrad && !good) n = 0;  // a bad group's gradient is left as it was
     }
-    s_scan[e] = n;
-    __syncthreads();
-    for (int d = 1; d < kThreads; d *= 2) {
-      const int add = e >= d ? s_scan[e - d] : 0;
-      __syncthreads();
-      s_scan[e] += add;
-      __syncthreads();
+    // inclusive sums: within each warp, then over the warps
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int up = __shfl_up_sync(0xffffffffu, n, d);
+      if (lane >= d) n += up;
     }
+    if (lane == 31) s_scan[warp] = n;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) n += s_scan[i];
     if (e == 0) s_pre[0] = 0;
-    if (e < p.groups) s_pre[e + 1] = s_scan[e];
+    if (e < p.groups) s_pre[e + 1] = n;
   }
   tc_fence_before();
   __syncthreads();
@@ -428,13 +493,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;  // TMEM lane quarter this warp may access
-    uint8_t* st = staging + q * 2048;
+    const int half = (warp - 4) >> 2;  // chunks of 32 r's: even or odd ones
+    const uint32_t st = smem_u32(staging) + (warp - 4) * Tr::kWarpStaging;
     int e = 0, it = 0;
     for (int w = first; w < W; w += step) {
       const GTile t = tile_of<M, Tr::kTileC, NB>(p, s_rows, s_pre, w, e);
       const int cw = t.c0 + int(rank) * ROWS_A + q * 32;
-      const int c = cw + lane;
-      const bool cvalid = q * 32 < ROWS_A && c < p.C;
       const long long row = M == kWgrad ? t.r0 : (long long)(t.row0) + t.r0;
       const long long base = (M == kWgrad ? t.e * p.group_stride : 0) + row * p.ldo;
       const int ab = it & 1;
@@ -447,18 +511,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       const uint32_t tb = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(ab * NB);
+      const bool mine = q * 32 < ROWS_A && cw < p.C;  // the warp has c's to store
 #pragma unroll 1
-      for (int j0 = 0; j0 < t.nr; j0 += 32) {
-        uint32_t r[32];
-        if (t.nk > 0) {
-          tmem_ld_32x32b_x32(tb + uint32_t(j0), r);
-          tmem_ld_wait();
-        } else {  // an empty group's gradient
-#pragma unroll
-          for (int j = 0; j < 32; ++j) r[j] = 0u;
+      for (int j0 = half * 32; j0 < t.nr && mine; j0 += 64) {
+        // the bulk store of the chunk before has read the staging tile
+        const bool bulk = M == kWgrad && p.tma_out;
+        if (bulk) {
+          if (lane == 0) bulk_wait_read();
+          __syncwarp();
         }
-        if (q * 32 < ROWS_A && cw < p.C)
-          store_chunk(p, r, st, base + j0 * p.ldo, c, cw, t.nr - j0, cvalid);
+        if constexpr (EB == 4) {
+          uint32_t r[32];
+          if (t.nk > 0) {
+            tmem_ld_32x32b_x32(tb + uint32_t(j0), r);
+            tmem_ld_wait();
+          } else {  // an empty group's gradient
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = 0u;
+          }
+          if (bulk)
+            stage_chunk_32(r, st);
+          else if (cw + lane < p.C)
+            store_chunk_32(p, r, static_cast<float*>(p.out) + base + j0 * p.ldo + cw + lane,
+                           t.nr - j0);
+        } else {
+          uint32_t r[2][16];
+          if (t.nk > 0) {
+            tmem_ld_16x256b_x4(tb + uint32_t(j0), r[0]);
+            tmem_ld_16x256b_x4(tb + (16u << 16) + uint32_t(j0), r[1]);
+            tmem_ld_wait_regs(r);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) r[0][j] = r[1][j] = 0u;
+          }
+          stage_chunk_16(p, r, st);
+          if (!bulk) {
+            __syncwarp();
+            store_chunk_16(p, st, static_cast<uint16_t*>(p.out) + base + j0 * p.ldo, cw,
+                           t.nr - j0);
+            __syncwarp();
+          }
+        }
+        if (bulk) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&p.tmO, st, cw, t.r0 + j0, t.e);
+            bulk_commit();
+          }
+        }
       }
       if (t.nk > 0) {
         tc_fence_before();
@@ -471,6 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    if (M == kWgrad && lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -487,15 +589,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <Mode M, int CG, int ROWS_A, int NB, int KPS, int STAGES>
+template <Mode M, int CG, int ROWS_A, int NB, int KPS, int STAGES, int EB>
 struct Variant {
-  using Tr = Traits<M, CG, ROWS_A, NB, KPS, STAGES>;
+  using Tr = Traits<M, CG, ROWS_A, NB, KPS, STAGES, EB>;
 
   static cudaError_t launch(const GroupedArgs& a, int dev, int sms, long long max_tiles,
                             cudaStream_t stream) {
     // the shared memory limit, once per device
     static std::atomic<bool> ready[kMaxDevices];
-    auto* fn = ragged_gemm_kernel<M, CG, ROWS_A, NB, KPS, STAGES>;
+    auto* fn = ragged_gemm_kernel<M, CG, ROWS_A, NB, KPS, STAGES, EB>;
     if (!ready[dev].load(std::memory_order_acquire)) {
       const cudaError_t e =
           cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Tr::kSmem);
@@ -539,13 +641,20 @@ bool map_of(CUtensorMap* m, const Operand& o, uint32_t fmt, int box_rows) {
                      uint32_t(box_rows));
 }
 
-template <Mode M, int CG, int ROWS_A, int NB, int KPS, int STAGES>
+template <Mode M, int CG, int ROWS_A, int NB, int KPS, int STAGES, int EB>
 moe_status run_variant(GroupedArgs& a, const Operand& A, const Operand& B, int dev, int sms,
                        cudaStream_t stream) {
-  using V = Variant<M, CG, ROWS_A, NB, KPS, STAGES>;
+  using V = Variant<M, CG, ROWS_A, NB, KPS, STAGES, EB>;
   bool ok = map_of(&a.tmA, A, a.fmt, M == kFwd ? ROWS_A : 64);
   ok = ok && map_of(&a.tmB, B, a.fmt, M == kWgrad ? 64 : NB / CG);
   if (M != kWgrad) ok = ok && map_of(&a.tmBs, B, a.fmt, kSmallBox);
+  if (M == kWgrad && a.tma_out)
+    ok = ok && make_map_3d(&a.tmO,
+                           EB == 4  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                           : a.fmt  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                           EB, a.out, uint64_t(a.C), uint64_t(a.R), uint64_t(a.groups),
+                           uint64_t(a.ldo) * EB, uint64_t(a.group_stride) * EB, 32, 32 * EB);
   if (!ok) return MOE_ERR_CUDA;
   if (V::launch(a, dev, sms, V::tiles_of(a), stream) != cudaSuccess) {
     cudaGetLastError();
@@ -572,15 +681,18 @@ bool bad_ld(int64_t ld, int width, bool tma) {
 }
 
 template <Mode M>
-moe_status dispatch(GroupedArgs& a, const Operand& A, const Operand& B, cudaStream_t stream) {
+moe_status dispatch(GroupedArgs& a, const Operand& A, const Operand& B, bool out_f32,
+                    cudaStream_t stream) {
   int dev = 0, sms = 0;
   const moe_status st = current_device(&dev, &sms);
   if (st != MOE_OK) return st;
   if constexpr (M != kWgrad) {
     if (a.rows <= 32LL * a.groups)
-      return run_variant<M, 1, 64, 64, 4, 3>(a, A, B, dev, sms, stream);
+      return run_variant<M, 1, 64, 64, 4, 3, 2>(a, A, B, dev, sms, stream);
+  } else {
+    if (out_f32) return run_variant<M, 2, 128, 256, 1, 5, 4>(a, A, B, dev, sms, stream);
   }
-  return run_variant<M, 2, 128, 256, 1, 6>(a, A, B, dev, sms, stream);
+  return run_variant<M, 2, 128, 256, 1, 6, 2>(a, A, B, dev, sms, stream);
 }
 
 }  // namespace
@@ -617,7 +729,7 @@ extern "C" moe_status moe_grouped_gemm(const void* x, int64_t ldx, const void* w
   a.vec = aligned_to(y, 16) && (ldy & 7) == 0;
   a.status = status;
   return moe::dispatch<moe::kFwd>(a, {w, ldw, in_features, out_features, num_experts},
-                                  {x, ldx, in_features, rows, 1},
+                                  {x, ldx, in_features, rows, 1}, false,
                                   static_cast<cudaStream_t>(stream));
 }
 
@@ -648,7 +760,7 @@ extern "C" moe_status moe_grouped_gemm_dgrad(const void* dy, int64_t lddy, const
   a.vec = aligned_to(dx, 16) && (lddx & 7) == 0;
   a.status = status;
   return moe::dispatch<moe::kDgrad>(a, {w, ldw, in_features, out_features, num_experts},
-                                    {dy, lddy, out_features, rows, 1},
+                                    {dy, lddy, out_features, rows, 1}, false,
                                     static_cast<cudaStream_t>(stream));
 }
 
@@ -681,9 +793,11 @@ extern "C" moe_status moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const
   a.ldo = lddw;
   a.group_stride = (long long)(out_features)*lddw;
   a.fmt = dtype == MOE_DTYPE_BF16;
-  a.out_f32 = f32;
   a.accumulate = accumulate;
   a.vec = !f32 && aligned_to(dw, 16) && (lddw & 7) == 0;
+  // a group's stride below TMA's 2^40 bytes too
+  a.tma_out = !accumulate && aligned_to(dw, 16) && (lddw * (f32 ? 4 : 2)) % 16 == 0 &&
+              a.group_stride < (1LL << 37);
   a.status = status;
   // no rows: every group is empty and no map is read through; the maps still
   // want a valid, aligned address
@@ -691,5 +805,5 @@ extern "C" moe_status moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const
   if (rows == 0) dy = x = none;
   const int r = rows > 0 ? rows : 1;
   return moe::dispatch<moe::kWgrad>(a, {x, ldx, in_features, r, 1}, {dy, lddy, out_features, r, 1},
-                                    static_cast<cudaStream_t>(stream));
+                                    f32, static_cast<cudaStream_t>(stream));
 }

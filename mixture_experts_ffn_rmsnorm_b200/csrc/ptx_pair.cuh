@@ -75,6 +75,30 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// 3-D tiled store of one box from shared memory, in this thread's current
+// bulk group; parts beyond the tensor's extents are not written.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x,
+                                             int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// Wait until this thread's bulk groups have read their shared memory / are
+// complete.
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 template <int CG>
 __device__ __forceinline__ void tmem_alloc_cg(uint32_t* dst, uint32_t ncols) {
   if constexpr (CG == 2) {
@@ -123,6 +147,31 @@ __device__ __forceinline__ void umma_commit_cg(uint64_t* bar) {
         : "memory");
   else
     umma_commit(bar);
+}
+
+// 16 lanes x 32 consecutive 32-bit TMEM columns in the fragment layout of
+// 8 x 8 matrices: thread T holds, for column block i of 8, lane T / 4 of
+// columns 8 i + 2 (T % 4) and the next in r[4 i], r[4 i + 1] and lane
+// T / 4 + 8 of the same columns in r[4 i + 2], r[4 i + 3].
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit elements, each stored transposed: thread T's
+// m[i] holds elements (rows 2 (T % 4) and the next, column T / 4) of matrix i
+// as they lie in memory; lane 8 i + r gives the address of matrix i's row r.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t m0, uint32_t m1,
+                                                  uint32_t m2, uint32_t m3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(m0), "r"(m1), "r"(m2), "r"(m3)
+               : "memory");
 }
 
 // Makes this thread's shared-memory stores visible to the async proxy
