@@ -329,6 +329,52 @@ MOE_API moe_status moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const vo
                                           void* dw, int64_t lddw, int32_t out_dtype,
                                           int32_t accumulate, int32_t* status, void* stream);
 
+/* Bounds of moe_nvfp4_gemv: routed rows (num_tokens * top_k) and in_features. */
+#define MOE_NVFP4_MAX_ROWS 1024
+#define MOE_NVFP4_MAX_K 8192
+
+/* Matrix-vector products of a few tokens with their experts' NVFP4 matrices
+ * (W4A16): a decode step's expert projections on 4-bit weights.
+ *
+ *   y[t, j, n] = act(s2[e] * sum_k E2M1(w[e, n, k]) * E4M3(s[e, n, k / 16]) * x[.., k]),
+ *   e = idx[t, j].  K = in_features, N = out_features, k = top_k; device memory.
+ *
+ *   x  [num_tokens, K], or with x_per_slot = 1 [num_tokens * k, K] (row
+ *      t * k + j for slot j); BF16 or FP16 (dtype); ldx elements apart.
+ *   idx [num_tokens, k] int32, as moe_route writes it.  An id may repeat.  The
+ *      row of an id outside [0, num_experts) becomes zero.
+ *   w  [E, N, K / 2]: two E2M1 codes (sign, two exponent bits, one mantissa
+ *      bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6) a byte, the even k in the low nibble.
+ *   w_scale [E, N, K / 16] E4M3, one per 16 inputs; w_scale2 [E] float32.
+ *   y  [num_tokens * k, N] of x's type, ldy elements apart.
+ *   activation: MOE_ACT_NONE or MOE_ACT_RELU2.
+ *   status: optional device int32, OR-ed into (the caller zeroes it): bit 2
+ *      for an id outside [0, num_experts), bit 1 if a wait timed out.
+ * Weights times scales are exact on the tensor cores, sums are float32, the
+ * result is rounded once.  The weights are read once per 8 rows of an expert.
+ *
+ * The call keeps no state and uses no workspace: it allocates nothing, may be
+ * captured in a CUDA graph and may overlap in time with others.  y must not
+ * overlap an operand.  The first call on a device does set-up; make it before
+ * any stream capture.
+ *
+ * Errors (nothing is launched): MOE_ERR_INVALID_CONFIG for num_experts outside
+ * [1, MOE_MAX_EXPERTS], top_k outside [1, MOE_MAX_TOP_K], K outside
+ * [32, MOE_NVFP4_MAX_K] or no multiple of 32, N outside
+ * [1, MOE_GROUPED_MAX_FEATURES], a bad dtype, activation or x_per_slot, ldx
+ * below K or no multiple of 8, or ldy below N; MOE_ERR_TOKENS_OUT_OF_RANGE
+ * for num_tokens < 0 or num_tokens * top_k above MOE_NVFP4_MAX_ROWS;
+ * MOE_ERR_NULL_POINTER; MOE_ERR_MISALIGNED for x, w or w_scale off a 16-byte
+ * boundary or another pointer off its element's; MOE_ERR_DEVICE if the
+ * current device is not sm_100; MOE_ERR_CUDA if the launch fails.
+ * num_tokens = 0 does nothing. */
+MOE_API moe_status moe_nvfp4_gemv(const void* x, int64_t ldx, int32_t x_per_slot,
+                                  const int32_t* idx, int32_t num_tokens, int32_t top_k,
+                                  const void* w, const void* w_scale, const float* w_scale2,
+                                  int32_t num_experts, int32_t in_features, int32_t out_features,
+                                  int32_t dtype, int32_t activation, void* y, int64_t ldy,
+                                  int32_t* status, void* stream);
+
 /* Copy the routing used by the last moe_forward* call on this handle (either
  * path) into idx [T, k] int32 and w [T, k] float32 (device pointers, same
  * meaning as moe_route's outputs); num_tokens must equal that call's. */

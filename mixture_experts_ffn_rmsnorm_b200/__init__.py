@@ -12,7 +12,7 @@ import os
 from typing import Optional
 
 __all__ = ["load_library", "sort_static", "grouped_gemm", "grouped_gemm_dgrad",
-           "grouped_gemm_wgrad", "MoEConfig", "MoELayer", "MoEError", "STATUS",
+           "grouped_gemm_wgrad", "nvfp4_gemv", "MoEConfig", "MoELayer", "MoEError", "STATUS",
            "PATH_AUTO", "PATH_DECODE", "PATH_PREFILL", "EXPORTED_SYMBOLS", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_b200.so")
@@ -30,7 +30,7 @@ EXPORTED_SYMBOLS = ("moe_create", "moe_forward", "moe_forward_path", "moe_forwar
                     "moe_get_device_status", "moe_last_launch_count", "moe_copy_routing",
                     "moe_set_stage_events", "moe_sort_static", "moe_copy_sort",
                     "moe_last_path", "moe_grouped_gemm", "moe_grouped_gemm_dgrad",
-                    "moe_grouped_gemm_wgrad")
+                    "moe_grouped_gemm_wgrad", "moe_nvfp4_gemv")
 
 
 class MoEError(RuntimeError):
@@ -97,6 +97,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                    ctypes.c_int),
         "moe_grouped_gemm_wgrad": ([V, I64, V, I64, V, I32, I32, I32, I32, I32, V, I64, I32, I32,
                                     V, V], ctypes.c_int),
+        "moe_nvfp4_gemv": ([V, I64, I32, V, I32, I32, V, V, V, I32, I32, I32, I32, I32, V, I64, V,
+                            V], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -274,6 +276,47 @@ def grouped_gemm_wgrad(dy, x, off, dw, accumulate=False, status=None, stream=Non
     st = load_library().moe_grouped_gemm_wgrad(_ptr(dy), ldy, _ptr(x), ldx, _ptr(off), E, rows, K,
                                                N, dt, _ptr(dw), ldw, _dtype_code(dw, what),
                                                int(accumulate), _ptr(status), s)
+    if st != 0:
+        raise MoEError(st, what)
+
+
+def nvfp4_gemv(x, idx, w, w_scale, w_scale2, y, relu2=False, status=None, stream=None):
+    """moe_nvfp4_gemv: y[t, j] = act(W[idx[t, j]] @ x[t]) (or x[t, j]) with
+    experts in NVFP4, for a decode step's few tokens.
+
+    x [T, K], or [T, k, K] with a row per slot, BF16 or FP16; idx [T, k] int32;
+    w [E, N, K / 2] bytes (two E2M1 codes, the even input in the low nibble),
+    w_scale [E, N, K / 16] E4M3 (or their bytes), w_scale2 [E] float32;
+    y [T, k, N] of x's dtype.  relu2 applies max(v, 0)^2.  An id outside
+    [0, E) gives a zero row and bit 2 of status."""
+    what = "moe_nvfp4_gemv"
+    torch = _need_torch()
+    if idx.dim() != 2 or idx.dtype != torch.int32 or not idx.is_contiguous():
+        raise MoEError(1, f"{what}: idx is not a contiguous int32 tensor [T, k]")
+    T, k = idx.shape
+    if w.dim() != 3 or not (w.is_contiguous() and w_scale.is_contiguous()
+                            and w_scale2.is_contiguous()):
+        raise MoEError(1, f"{what}: w [E, N, K / 2], w_scale or w_scale2 is not contiguous")
+    E, N, half = w.shape
+    K = 2 * half
+    if w.dtype != torch.uint8 or w_scale.dtype not in (torch.uint8, torch.float8_e4m3fn) or (
+            w_scale2.dtype != torch.float32):
+        raise MoEError(1, f"{what}: dtypes {w.dtype}, {w_scale.dtype}, {w_scale2.dtype}")
+    per_slot = x.dim() == 3
+    if tuple(x.shape) != ((T, k, K) if per_slot else (T, K)) or tuple(y.shape) != (T, k, N) or (
+            tuple(w_scale.shape) != (E, N, K // 16) or w_scale2.numel() != E):
+        raise MoEError(1, f"{what}: shapes {tuple(x.shape)}, {tuple(idx.shape)}, {tuple(w.shape)}, "
+                          f"{tuple(w_scale.shape)}, {tuple(w_scale2.shape)}, {tuple(y.shape)}")
+    dt = _dtype_code(x, what)
+    if y.dtype != x.dtype:
+        raise MoEError(1, f"{what}: x and y have different dtypes")
+    ldx = _experts_ld(x, what, "x") if per_slot else _rows_ld(x, what, "x")
+    ldy = _experts_ld(y, what, "y")
+    _check_status(status, what)
+    s = _launch_stream(what, stream, x, idx, w, w_scale, w_scale2, y, status)
+    st = load_library().moe_nvfp4_gemv(_ptr(x), ldx, int(per_slot), _ptr(idx), T, k, _ptr(w),
+                                       _ptr(w_scale), _ptr(w_scale2), E, K, N, dt, int(relu2),
+                                       _ptr(y), ldy, _ptr(status), s)
     if st != 0:
         raise MoEError(st, what)
 

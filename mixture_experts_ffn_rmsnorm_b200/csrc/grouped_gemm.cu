@@ -47,13 +47,11 @@ constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 static_assert(kThreads >= MOE_MAX_EXPERTS, "one thread per group derives the tile list");
 constexpr int kBK = 64;        // elements of q per k-block (128 bytes)
-constexpr int kSmallBox = 16;  // rows of the small K-major box of B
 
 struct GroupedArgs {
-  CUtensorMap tmA;   // forward: 128-row (or kARows) boxes; else 64-row boxes
-  CUtensorMap tmB;   // K-major: NB / CG rows a box; weight gradient: 64
-  CUtensorMap tmBs;  // K-major B in boxes of kSmallBox rows
-  CUtensorMap tmO;   // weight gradient with `tma_out`: 32 x 32 boxes of the output
+  CUtensorMap tmA;     // forward: 128-row boxes; else 64-row boxes
+  CUtensorMap tmB[4];  // K-major: boxes of 16, 32, 64 and 128 rows; weight gradient: [0], 64
+  CUtensorMap tmO;     // weight gradient with `tma_out`: 32 x 32 boxes of the output
   const int* off;
   int groups;
   int rows;  // rows of the row tensors: no group may end behind it
@@ -65,28 +63,25 @@ struct GroupedArgs {
   long long group_stride;  // elements (weight gradient)
   uint32_t fmt;            // 0 = FP16, 1 = BF16
   int relu2;
+  int rgroup;  // r tiles of a unit (forward, data gradient)
   int accumulate;  // out += (FP32 only)
   int tma_out;     // weight gradient: whole chunks leave by TMA
   int vec;         // 16-byte stores: base, ldo and group_stride allow them
   int* status;
 };
 
-template <Mode M, int CG, int ROWS_A, int NB, int KPS, int STAGES, int EB>
+template <Mode M, int CG, int NB, int KPS, int STAGES, int EB>
 struct Traits {
   static constexpr bool kAMN = M != kFwd;
   static constexpr bool kBMN = M == kWgrad;
-  static constexpr int kABytes = ROWS_A * 128;       // one k-block of A in one CTA
+  static constexpr int kABytes = 128 * 128;          // one k-block of A in one CTA
   static constexpr int kBBytes = NB / CG * 128;      // one k-block of B in one CTA
   static constexpr int kStageBytes = KPS * (kABytes + kBBytes);
-  static constexpr int kTileC = ROWS_A * CG;
+  static constexpr int kTileC = 128 * CG;
   static constexpr int kTmemCols = 2 * NB;
   static constexpr int kWarpStaging = 32 * 32 * EB;  // one chunk of the epilogue
   static constexpr int kStagingBytes = kEpiWarps * kWarpStaging;
   static constexpr int kSmem = 1024 + STAGES * kStageBytes + kStagingBytes + 512;
-  static_assert(ROWS_A == 128 || (ROWS_A == 64 && CG == 1), "");
-  // an M = 128 MMA reads 128 rows of A: with 64 loaded rows the others lie in
-  // the B block behind them (their accumulator rows are not stored)
-  static_assert(ROWS_A == 128 || kBBytes >= 64 * 128, "");
   static_assert(!kBMN || KPS == 1, "the tail of a group is one k-block of one stage");
   static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols <= 512, "");
   static_assert(kSmem <= 232448 - 8192, "");  // beside the static tables
@@ -102,26 +97,45 @@ struct GTile {
   int nk;    // k-blocks
 };
 
-// Tile w of the launch.  `e` is a cursor: the calls of one thread come with
-// increasing w.  pre[e] = tiles of the groups before e.
+// The tiles of one CTA (pair), in order.  Work is handed out in units: one c
+// tile with up to `rgroup` r tiles of a group after one another, so that the
+// second finds the weights that the first brought in in L2.  Unit u goes to
+// CTA (pair) u mod step; pre[e] = units of the groups before e.
 template <Mode M, int TILE_C, int NB>
-__device__ __forceinline__ GTile tile_of(const GroupedArgs& p, const int* off, const int* pre,
-                                         int w, int& e) {
-  while (pre[e + 1] <= w) ++e;
+struct Walk {
+  int u, step, e = 0, more = 0;
   GTile t;
-  const int ct = (p.C + TILE_C - 1) / TILE_C;
-  const int i = w - pre[e];
-  const int ri = i / ct;
-  t.e = e;
-  t.row0 = off[2 * e];
-  t.cnt = off[2 * e + 1];
-  t.c0 = (i - ri * ct) * TILE_C;
-  t.r0 = ri * NB;
-  const int ext = M == kWgrad ? p.R : t.cnt;
-  t.nr = min(NB, ext - t.r0);
-  t.nk = ((M == kWgrad ? t.cnt : p.Q) + kBK - 1) / kBK;
-  return t;
-}
+
+  __device__ __forceinline__ Walk(int first, int step_) : u(first), step(step_) {}
+
+  __device__ __forceinline__ bool next(const GroupedArgs& p, const int* off, const int* pre,
+                                       int rgroup) {
+    if (more > 0) {
+      --more;
+      t.r0 += NB;
+    } else {
+      if (u >= pre[p.groups]) return false;
+      while (pre[e + 1] <= u) ++e;
+      const int ct = (p.C + TILE_C - 1) / TILE_C;
+      const int i = u - pre[e];
+      const int rg = i / ct;
+      t.e = e;
+      t.row0 = off[2 * e];
+      t.cnt = off[2 * e + 1];
+      t.c0 = (i - rg * ct) * TILE_C;
+      t.r0 = rg * rgroup * NB;
+      t.nk = ((M == kWgrad ? t.cnt : p.Q) + kBK - 1) / kBK;
+      const int left = (ext(p) - t.r0 + NB - 1) / NB;
+      more = min(rgroup, left) - 1;
+      u += step;
+    }
+    t.nr = min(NB, ext(p) - t.r0);
+    return true;
+  }
+  __device__ __forceinline__ int ext(const GroupedArgs& p) const {
+    return M == kWgrad ? p.R : t.cnt;
+  }
+};
 
 __device__ __forceinline__ void give_up(const GroupedArgs& p, volatile int* abort) {
   *abort = 1;
@@ -241,10 +255,10 @@ __device__ __forceinline__ void store_chunk_32(const GroupedArgs& p, const uint3
   }
 }
 
-template <Mode M, int CG, int ROWS_A, int NB, int KPS, int STAGES, int EB>
+template <Mode M, int CG, int NB, int KPS, int STAGES, int EB>
 __global__ void __launch_bounds__(kThreads, 1)
     ragged_gemm_kernel(const __grid_constant__ GroupedArgs p) {
-  using Tr = Traits<M, CG, ROWS_A, NB, KPS, STAGES, EB>;
+  using Tr = Traits<M, CG, NB, KPS, STAGES, EB>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* tiles = smem_raw + pad;
@@ -280,11 +294,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort = 0;
     fence_barrier_init();
     tma_prefetch_desc(&p.tmA);
-    tma_prefetch_desc(&p.tmB);
+    tma_prefetch_desc(&p.tmB[0]);
   }
   if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, Tr::kTmemCols);
 
-  // the tile list: tiles of each group, prefix sums
+  // the work list: units of each group, prefix sums
+  const int rgroup = M == kWgrad ? 1 : p.rgroup;
   {
     const int ct = (p.C + Tr::kTileC - 1) / Tr::kTileC;
     const int e = threadIdx.x;
@@ -296,7 +311,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cnt = good ? b - a : 0;
       s_rows[2 * e] = good ? a : 0;
       s_rows[2 * e + 1] = cnt;
-      n = ((M == kWgrad ? p.R : cnt) + NB - 1) / NB * ct;
+      const int rt = ((M == kWgrad ? p.R : cnt) + NB - 1) / NB;
+      n = (rt + rgroup - 1) / rgroup * ct;
       if (M == kWgrad && cnt == 0 && p.accumulate) n = 0;  // nothing to add
       if (M == kWgrad && !good) n = 0;  // a bad group's gradient is left as it was
     }
@@ -317,32 +333,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int W = s_pre[p.groups];
-  const int step = int(gridDim.x) / CG;
-  const int first = int(blockIdx.x) / CG;
+  Walk<M, Tr::kTileC, NB> walk(int(blockIdx.x) / CG, int(gridDim.x) / CG);
   const uint32_t tiles_u32 = smem_u32(tiles);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int stage = 0, e = 0;
+      int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int w = first; w < W && ok; w += step) {
-        const GTile t = tile_of<M, Tr::kTileC, NB>(p, s_rows, s_pre, w, e);
+      while (ok && walk.next(p, s_rows, s_pre, rgroup)) {
+        const GTile& t = walk.t;
         const int nmma = (t.nr + 15) & ~15;
         const int nb = nmma / CG;  // r's of B this CTA loads
-        const int ca = t.c0 + int(rank) * ROWS_A;
+        const int ca = t.c0 + int(rank) * 128;
         const int rb = t.r0 + int(rank) * nb;
-        int nbox;  // boxes of B per k-block
+        // B of one k-block: one K-major box of 16, 32, 64 or 128 rows (several
+        // smaller ones cost more than the rows they save), or MN-major boxes
+        // of 64
+        int nbox = 1, size = 0;
         uint32_t bbytes;
         if (Tr::kBMN) {
           nbox = (nb + 63) / 64;
           bbytes = nbox * 64 * 128;
         } else {
-          nbox = (nb + kSmallBox - 1) / kSmallBox;
-          if (nbox * 2 > NB / CG / kSmallBox) nbox = 0;  // one large box
-          bbytes = nbox ? nbox * kSmallBox * 128 : Tr::kBBytes;
+          size = nb <= 16 ? 0 : nb <= 32 ? 1 : nb <= 64 ? 2 : 3;
+          bbytes = 2048u << size;
         }
         for (int kb0 = 0; kb0 < t.nk; kb0 += KPS) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort)) {
@@ -374,18 +390,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int y = M == kDgrad ? kb * kBK : t.row0 + kb * kBK;
               const int z = M == kDgrad ? t.e : 0;
 #pragma unroll
-              for (int h = 0; h < ROWS_A / 64; ++h)
+              for (int h = 0; h < 2; ++h)
                 tma_load_3d<CG>(sa + h * 8192, &p.tmA, bar, ca + h * 64, y, z);
             }
             if constexpr (M == kWgrad) {
               for (int h = 0; h < nbox; ++h)
-                tma_load_3d<CG>(sb + h * 8192, &p.tmB, bar, rb + h * 64, t.row0 + kb * kBK, 0);
-            } else if (nbox == 0) {
-              tma_load_3d<CG>(sb, &p.tmB, bar, kb * kBK, t.row0 + rb, 0);
+                tma_load_3d<CG>(sb + h * 8192, &p.tmB[0], bar, rb + h * 64, t.row0 + kb * kBK, 0);
             } else {
-              for (int h = 0; h < nbox; ++h)
-                tma_load_3d<CG>(sb + h * kSmallBox * 128, &p.tmBs, bar, kb * kBK,
-                                t.row0 + rb + h * kSmallBox, 0);
+              tma_load_3d<CG>(sb, &p.tmB[size], bar, kb * kBK, t.row0 + rb, 0);
             }
           }
           if (++stage == STAGES) {
@@ -403,11 +415,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     if (lane == 0 && rank == 0) {
-      int stage = 0, e = 0, it = 0;
+      int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int w = first; w < W && ok; w += step) {
-        const GTile t = tile_of<M, Tr::kTileC, NB>(p, s_rows, s_pre, w, e);
+      while (ok && walk.next(p, s_rows, s_pre, rgroup)) {
+        const GTile& t = walk.t;
         if (t.nk == 0) continue;
         const int nmma = (t.nr + 15) & ~15;
         const uint32_t idesc = make_idesc_16(128 * CG, nmma, p.fmt, Tr::kAMN, Tr::kBMN);
@@ -461,10 +473,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (M == kWgrad && warp == 2) {
     // ---------------------------------------- rows behind a group's last one
-    int e = 0, total = 0;
+    int total = 0;
     uint32_t used = 0;  // phase bit of each stage's tail barrier
-    for (int w = first; w < W; w += step) {
-      const GTile t = tile_of<M, Tr::kTileC, NB>(p, s_rows, s_pre, w, e);
+    while (walk.next(p, s_rows, s_pre, rgroup)) {
+      const GTile& t = walk.t;
       total += t.nk;
       const int valid = t.cnt & (kBK - 1);
       if (valid == 0) continue;
@@ -475,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       used ^= 1u << stage;
       const int nb = ((t.nr + 15) & ~15) / CG;
-      const int blocks = ROWS_A / 64 + (nb + 63) / 64;
+      const int blocks = 2 + (nb + 63) / 64;
       const int end = (valid + 15) & ~15;
       for (int h = 0; h < blocks; ++h) {
         uint32_t* blk = reinterpret_cast<uint32_t*>(tiles + stage * Tr::kStageBytes + h * 8192);
@@ -495,10 +507,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3;  // TMEM lane quarter this warp may access
     const int half = (warp - 4) >> 2;  // chunks of 32 r's: even or odd ones
     const uint32_t st = smem_u32(staging) + (warp - 4) * Tr::kWarpStaging;
-    int e = 0, it = 0;
-    for (int w = first; w < W; w += step) {
-      const GTile t = tile_of<M, Tr::kTileC, NB>(p, s_rows, s_pre, w, e);
-      const int cw = t.c0 + int(rank) * ROWS_A + q * 32;
+    int it = 0;
+    while (walk.next(p, s_rows, s_pre, rgroup)) {
+      const GTile& t = walk.t;
+      const int cw = t.c0 + int(rank) * 128 + q * 32;
       const long long row = M == kWgrad ? t.r0 : (long long)(t.row0) + t.r0;
       const long long base = (M == kWgrad ? t.e * p.group_stride : 0) + row * p.ldo;
       const int ab = it & 1;
@@ -511,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       const uint32_t tb = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(ab * NB);
-      const bool mine = q * 32 < ROWS_A && cw < p.C;  // the warp has c's to store
+      const bool mine = cw < p.C;  // the warp has c's to store
 #pragma unroll 1
       for (int j0 = half * 32; j0 < t.nr && mine; j0 += 64) {
         // the bulk store of the chunk before has read the staging tile
@@ -589,15 +601,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <Mode M, int CG, int ROWS_A, int NB, int KPS, int STAGES, int EB>
+template <Mode M, int CG, int NB, int KPS, int STAGES, int EB>
 struct Variant {
-  using Tr = Traits<M, CG, ROWS_A, NB, KPS, STAGES, EB>;
+  using Tr = Traits<M, CG, NB, KPS, STAGES, EB>;
 
   static cudaError_t launch(const GroupedArgs& a, int dev, int sms, long long max_tiles,
                             cudaStream_t stream) {
     // the shared memory limit, once per device
     static std::atomic<bool> ready[kMaxDevices];
-    auto* fn = ragged_gemm_kernel<M, CG, ROWS_A, NB, KPS, STAGES, EB>;
+    auto* fn = ragged_gemm_kernel<M, CG, NB, KPS, STAGES, EB>;
     if (!ready[dev].load(std::memory_order_acquire)) {
       const cudaError_t e =
           cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Tr::kSmem);
@@ -641,13 +653,16 @@ bool map_of(CUtensorMap* m, const Operand& o, uint32_t fmt, int box_rows) {
                      uint32_t(box_rows));
 }
 
-template <Mode M, int CG, int ROWS_A, int NB, int KPS, int STAGES, int EB>
+template <Mode M, int CG, int NB, int KPS, int STAGES, int EB>
 moe_status run_variant(GroupedArgs& a, const Operand& A, const Operand& B, int dev, int sms,
                        cudaStream_t stream) {
-  using V = Variant<M, CG, ROWS_A, NB, KPS, STAGES, EB>;
-  bool ok = map_of(&a.tmA, A, a.fmt, M == kFwd ? ROWS_A : 64);
-  ok = ok && map_of(&a.tmB, B, a.fmt, M == kWgrad ? 64 : NB / CG);
-  if (M != kWgrad) ok = ok && map_of(&a.tmBs, B, a.fmt, kSmallBox);
+  using V = Variant<M, CG, NB, KPS, STAGES, EB>;
+  bool ok = map_of(&a.tmA, A, a.fmt, M == kFwd ? 128 : 64);
+  if (M == kWgrad)
+    ok = ok && map_of(&a.tmB[0], B, a.fmt, 64);
+  else
+    for (int i = 0; i < 4 && (16 << i) <= NB / CG; ++i)
+      ok = ok && map_of(&a.tmB[i], B, a.fmt, 16 << i);
   if (M == kWgrad && a.tma_out)
     ok = ok && make_map_3d(&a.tmO,
                            EB == 4  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
@@ -687,12 +702,15 @@ moe_status dispatch(GroupedArgs& a, const Operand& A, const Operand& B, bool out
   const moe_status st = current_device(&dev, &sms);
   if (st != MOE_OK) return st;
   if constexpr (M != kWgrad) {
-    if (a.rows <= 32LL * a.groups)
-      return run_variant<M, 1, 64, 64, 4, 3, 2>(a, A, B, dev, sms, stream);
+    a.rgroup = 1;
+    if (a.rows <= 64LL * a.groups) return run_variant<M, 1, 64, 2, 4, 2>(a, A, B, dev, sms, stream);
+    if (a.rows <= 128LL * a.groups)
+      return run_variant<M, 2, 128, 2, 4, 2>(a, A, B, dev, sms, stream);
+    return run_variant<M, 2, 256, 2, 3, 2>(a, A, B, dev, sms, stream);
   } else {
-    if (out_f32) return run_variant<M, 2, 128, 256, 1, 5, 4>(a, A, B, dev, sms, stream);
+    if (out_f32) return run_variant<M, 2, 256, 1, 5, 4>(a, A, B, dev, sms, stream);
+    return run_variant<M, 2, 256, 1, 6, 2>(a, A, B, dev, sms, stream);
   }
-  return run_variant<M, 2, 128, 256, 1, 6, 2>(a, A, B, dev, sms, stream);
 }
 
 }  // namespace

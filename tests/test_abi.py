@@ -183,3 +183,24 @@ def test_grouped_gemm_validates_on_host():
     assert wgrad(odt=2, dw=258) == 3  # float32 elements
     assert fwd(rows=0, x=None, y=None) == 0   # nothing to do
     assert dgrad(rows=0, dy=None, dx=None) == 0
+
+
+def test_nvfp4_gemv_validates_on_host():
+    lib = moe.load_library()
+    p = 256
+
+    def gemv(x=p, ldx=64, per_slot=0, idx=p, T=2, k=3, w=p, ws=p, ws2=p, E=4, K=64, N=24, dt=0,
+             act=0, y=p, ldy=24):
+        return lib.moe_nvfp4_gemv(x, ldx, per_slot, idx, T, k, w, ws, ws2, E, K, N, dt, act, y, ldy,
+                                  None, None)
+
+    for name in ("x", "idx", "w", "ws", "ws2", "y"):
+        assert gemv(**{name: None}) == 2, name
+        assert gemv(**{name: 257}) == 3, name
+    for bad in (dict(E=0), dict(E=257), dict(k=0), dict(k=17), dict(K=0), dict(K=48), dict(K=8224),
+                dict(N=0), dict(N=131073), dict(dt=2), dict(act=2), dict(per_slot=2), dict(ldx=56),
+                dict(ldx=66), dict(ldy=23)):
+        assert gemv(**bad) == 1, bad
+    assert gemv(T=-1) == 4
+    assert gemv(T=342) == 4  # 1026 routed rows
+    assert gemv(T=0, x=None, y=None) == 0
