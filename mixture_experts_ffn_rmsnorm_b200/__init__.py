@@ -134,14 +134,19 @@ def sort_static(idx, top_k, num_experts, perm, inv, off, status=None, stream=Non
 
 _torch = None
 _DTYPES = {}  # torch dtype -> moe_dtype
+_current_device = _raw_stream = None
 
 
 def _need_torch():
     """torch, imported at the first call (the binding itself does without)."""
-    global _torch
+    global _torch, _current_device, _raw_stream
     if _torch is None:
         import torch
         _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+        _current_device = torch.cuda.current_device
+        # the current stream's handle without a Stream object (3 us less a call)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
         _torch = torch
     return _torch
 
@@ -156,14 +161,17 @@ def _dtype_code(t, what) -> int:
 def _launch_stream(what, stream, *tensors) -> Optional[int]:
     """The stream to launch on; all tensors lie on the current CUDA device,
     where the library launches."""
-    s = _torch.cuda.current_stream() if stream is None else stream
-    cur = s.device
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != cur:
-            raise MoEError(7, f"{what}: a tensor is on {t.device}, not on {cur}")
-    if stream is not None and cur.index != _torch.cuda.current_device():
-        raise MoEError(7, f"{what}: the stream is on {cur}, which is not the current device")
-    return s.cuda_stream or None
+        if t is not None and t.get_device() != dev:
+            raise MoEError(7, f"{what}: tensors on different devices")
+    if dev < 0 or dev != _current_device():
+        raise MoEError(7, f"{what}: the tensors are not on the current CUDA device")
+    if stream is None:
+        return _raw_stream(dev) or None
+    if stream.device.index != dev:
+        raise MoEError(7, f"{what}: the stream is on {stream.device}")
+    return stream.cuda_stream or None
 
 
 def _rows_ld(t, what, name) -> int:
@@ -215,7 +223,7 @@ def grouped_gemm(x, w, off, y, relu2=False, status=None, stream=None):
     ldx, ldw, ldy = _rows_ld(x, what, "x"), _experts_ld(w, what, "w"), _rows_ld(y, what, "y")
     E, N, K = w.shape
     rows = x.shape[0]
-    if x.shape[1] != K or tuple(y.shape) != (rows, N):
+    if x.shape[1] != K or y.shape != (rows, N):
         raise MoEError(1, f"{what}: shapes {tuple(x.shape)}, {tuple(w.shape)}, {tuple(y.shape)}")
     dt = _dtype_code(x, what)
     if w.dtype != x.dtype or y.dtype != x.dtype:
@@ -223,7 +231,7 @@ def grouped_gemm(x, w, off, y, relu2=False, status=None, stream=None):
     _check_off(off, E, what)
     _check_status(status, what)
     s = _launch_stream(what, stream, x, w, off, y, status)
-    st = load_library().moe_grouped_gemm(_ptr(x), ldx, _ptr(w), ldw, _ptr(off), E, rows, K, N, dt,
+    st = (_lib or load_library()).moe_grouped_gemm(_ptr(x), ldx, _ptr(w), ldw, _ptr(off), E, rows, K, N, dt,
                                          int(relu2), _ptr(y), ldy, _ptr(status), s)
     if st != 0:
         raise MoEError(st, what)
@@ -239,7 +247,7 @@ def grouped_gemm_dgrad(dy, w, off, dx, status=None, stream=None):
     ldy, ldw, ldx = _rows_ld(dy, what, "dy"), _experts_ld(w, what, "w"), _rows_ld(dx, what, "dx")
     E, N, K = w.shape
     rows = dy.shape[0]
-    if dy.shape[1] != N or tuple(dx.shape) != (rows, K):
+    if dy.shape[1] != N or dx.shape != (rows, K):
         raise MoEError(1, f"{what}: shapes {tuple(dy.shape)}, {tuple(w.shape)}, {tuple(dx.shape)}")
     dt = _dtype_code(dy, what)
     if w.dtype != dy.dtype or dx.dtype != dy.dtype:
@@ -247,7 +255,7 @@ def grouped_gemm_dgrad(dy, w, off, dx, status=None, stream=None):
     _check_off(off, E, what)
     _check_status(status, what)
     s = _launch_stream(what, stream, dy, w, off, dx, status)
-    st = load_library().moe_grouped_gemm_dgrad(_ptr(dy), ldy, _ptr(w), ldw, _ptr(off), E, rows, K,
+    st = (_lib or load_library()).moe_grouped_gemm_dgrad(_ptr(dy), ldy, _ptr(w), ldw, _ptr(off), E, rows, K,
                                                N, dt, _ptr(dx), ldx, _ptr(status), s)
     if st != 0:
         raise MoEError(st, what)
@@ -265,7 +273,7 @@ def grouped_gemm_wgrad(dy, x, off, dw, accumulate=False, status=None, stream=Non
     ldy, ldx, ldw = _rows_ld(dy, what, "dy"), _rows_ld(x, what, "x"), _experts_ld(dw, what, "dw")
     E, N, K = dw.shape
     rows = dy.shape[0]
-    if dy.shape[1] != N or tuple(x.shape) != (rows, K):
+    if dy.shape[1] != N or x.shape != (rows, K):
         raise MoEError(1, f"{what}: shapes {tuple(dy.shape)}, {tuple(x.shape)}, {tuple(dw.shape)}")
     dt = _dtype_code(dy, what)
     if x.dtype != dy.dtype:
@@ -273,7 +281,7 @@ def grouped_gemm_wgrad(dy, x, off, dw, accumulate=False, status=None, stream=Non
     _check_off(off, E, what)
     _check_status(status, what)
     s = _launch_stream(what, stream, dy, x, off, dw, status)
-    st = load_library().moe_grouped_gemm_wgrad(_ptr(dy), ldy, _ptr(x), ldx, _ptr(off), E, rows, K,
+    st = (_lib or load_library()).moe_grouped_gemm_wgrad(_ptr(dy), ldy, _ptr(x), ldx, _ptr(off), E, rows, K,
                                                N, dt, _ptr(dw), ldw, _dtype_code(dw, what),
                                                int(accumulate), _ptr(status), s)
     if st != 0:
@@ -303,8 +311,8 @@ def nvfp4_gemv(x, idx, w, w_scale, w_scale2, y, relu2=False, status=None, stream
             w_scale2.dtype != torch.float32):
         raise MoEError(1, f"{what}: dtypes {w.dtype}, {w_scale.dtype}, {w_scale2.dtype}")
     per_slot = x.dim() == 3
-    if tuple(x.shape) != ((T, k, K) if per_slot else (T, K)) or tuple(y.shape) != (T, k, N) or (
-            tuple(w_scale.shape) != (E, N, K // 16) or w_scale2.numel() != E):
+    if x.shape != ((T, k, K) if per_slot else (T, K)) or y.shape != (T, k, N) or (
+            w_scale.shape != (E, N, K // 16) or w_scale2.numel() != E):
         raise MoEError(1, f"{what}: shapes {tuple(x.shape)}, {tuple(idx.shape)}, {tuple(w.shape)}, "
                           f"{tuple(w_scale.shape)}, {tuple(w_scale2.shape)}, {tuple(y.shape)}")
     dt = _dtype_code(x, what)
@@ -314,7 +322,7 @@ def nvfp4_gemv(x, idx, w, w_scale, w_scale2, y, relu2=False, status=None, stream
     ldy = _experts_ld(y, what, "y")
     _check_status(status, what)
     s = _launch_stream(what, stream, x, idx, w, w_scale, w_scale2, y, status)
-    st = load_library().moe_nvfp4_gemv(_ptr(x), ldx, int(per_slot), _ptr(idx), T, k, _ptr(w),
+    st = (_lib or load_library()).moe_nvfp4_gemv(_ptr(x), ldx, int(per_slot), _ptr(idx), T, k, _ptr(w),
                                        _ptr(w_scale), _ptr(w_scale2), E, K, N, dt, int(relu2),
                                        _ptr(y), ldy, _ptr(status), s)
     if st != 0:

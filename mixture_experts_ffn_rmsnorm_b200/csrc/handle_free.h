@@ -82,4 +82,21 @@ inline bool make_map_3d(CUtensorMap* m, CUtensorMapDataType type, uint32_t elem_
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3-D map of a byte matrix [rows, blocks * 128] as [blocks, rows, 128]: one
+// box = 16 rows x up to `blocks` (at most 256) spans of 128 bytes, each span
+// a tile of its own in shared memory (128-byte swizzle).
+inline bool make_map_spans(CUtensorMap* m, const void* base, uint64_t rows, uint64_t row_stride,
+                           uint32_t blocks, uint32_t box_rows) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {128, rows, blocks};
+  const cuuint64_t strides[2] = {row_stride, 128};
+  const cuuint32_t box[3] = {128, box_rows, blocks};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace moe

@@ -43,7 +43,8 @@ constexpr int kMaxRows = MOE_NVFP4_MAX_ROWS;
 constexpr int kGemvSmemMax = 232448;
 
 struct GemvArgs {
-  CUtensorMap tmW;  // [E * N, K / 2] bytes, boxes of 128 bytes x 16 rows
+  CUtensorMap tmW;  // [E * N, K / 2] bytes in spans of 128: a box is the whole spans of 16 rows
+  CUtensorMap tmT;  // the same as rows: a box is 128 bytes of 16 rows (the part of a span at the end)
   const void* x;
   long long ldx;
   int per_slot;
@@ -80,8 +81,7 @@ struct Setup {
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -110,14 +110,6 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -166,6 +158,104 @@ __device__ __forceinline__ uint4 scaled_f16(const uint4& u, float s) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+__device__ __forceinline__ int expert_of(const GemvArgs& p, int r) {
+  const int e = p.idx[r];
+  const bool good = unsigned(e) < unsigned(p.E);
+  if (!good && p.status && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
+  return good ? e : -1;
+}
+
+// The passes of up to 32 routed rows, by one warp with a row per lane (a
+// decode step's few tokens: nothing but shuffles between the ids' arrival and
+// the first weight load).
+__device__ __forceinline__ void group_few_rows(const GemvArgs& p, Setup& S) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t before = (1u << lane) - 1u;
+  const int e = lane < p.R ? expert_of(p, lane) : -1;
+  const uint32_t same = __match_any_sync(0xffffffffu, e);
+  const int rank = __popc(same & before), count = __popc(same);
+  const int chunk = rank / p.rp * p.rp;  // rank of the pass's first row
+  const uint32_t leaders = __ballot_sync(0xffffffffu, e >= 0 && rank == chunk);
+  uint32_t rest = same;
+  for (int i = 0; i < chunk; ++i) rest &= rest - 1;
+  const int pass = __popc(leaders & ((1u << (__ffs(rest) - 1)) - 1u));
+  if (lane < p.R) S.id[lane] = int16_t(e);
+  if (e >= 0) {
+    S.sorted[pass * p.rp + rank - chunk] = int16_t(lane);
+    if (rank == chunk) {
+      S.pass_e[pass] = uint8_t(e);
+      S.pass_at[pass] = int16_t(pass * p.rp);
+      S.pass_n[pass] = int16_t(min(p.rp, count - rank));
+    }
+  }
+  if (lane == 0) S.passes = __popc(leaders);
+}
+
+// The passes of any number of rows, by one warp; S.id is set and S.count zero.
+__device__ __forceinline__ void group_rows(const GemvArgs& p, Setup& S) {
+  const int lane = threadIdx.x & 31;
+  // rank of each row among the rows of its expert, in row order
+  for (int r0 = 0; r0 < p.R; r0 += 32) {
+    const int r = r0 + lane;
+    const int e = r < p.R ? S.id[r] : -1;
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    int rank = 0;
+    if (e >= 0) rank = S.count[e] + __popc(same & ((1u << lane) - 1u));
+    __syncwarp();
+    if (e >= 0 && (same >> lane) == 1u) S.count[e] = rank + 1;  // the highest lane
+    if (r < p.R) S.pass_n[r] = int16_t(rank);
+    __syncwarp();
+  }
+  // first sorted position and first pass of each expert
+  constexpr int kPer = MOE_MAX_EXPERTS / 32;
+  int rows[kPer], nr = 0, np = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    rows[i] = S.count[lane * kPer + i];
+    nr += rows[i];
+    np += (rows[i] + p.rp - 1) / p.rp;
+  }
+  int sr = nr, sp = np;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int a = __shfl_up_sync(0xffffffffu, sr, d), b = __shfl_up_sync(0xffffffffu, sp, d);
+    if (lane >= d) {
+      sr += a;
+      sp += b;
+    }
+  }
+  if (lane == 31) S.passes = sp;
+  int base = sr - nr, pass = sp - np;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    S.first[lane * kPer + i] = base;
+    base += rows[i];
+  }
+  __syncwarp();
+  for (int r = lane; r < p.R; r += 32) {
+    const int e = S.id[r];
+    if (e >= 0) S.sorted[S.first[e] + S.pass_n[r]] = int16_t(r);
+  }
+  __syncwarp();
+  base = sr - nr;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    for (int a = 0; a < rows[i]; a += p.rp, ++pass) {
+      S.pass_e[pass] = uint8_t(lane * kPer + i);
+      S.pass_at[pass] = int16_t(base + a);
+      S.pass_n[pass] = int16_t(min(p.rp, rows[i] - a));
+    }
+    base += rows[i];
+  }
+}
+
+// The operands of one 128-wide block that a lane takes from a stage: 32
+// weights of two rows and their two scales each, as f16 pairs.
+struct Block {
+  uint4 wa, wb;
+  uint32_t sa, sb;
+};
+
 template <bool BF16>
 __global__ void __launch_bounds__(kGemvThreads, 1)
     nvfp4_gemv_kernel(const __grid_constant__ GemvArgs p) {
@@ -189,79 +279,28 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     }
     fence_barrier_init();
     tma_prefetch_desc(&p.tmW);
-  }
-  // ---- passes: routed rows grouped by expert, at most rp rows each
-  for (int e = tid; e < MOE_MAX_EXPERTS; e += kGemvThreads) S.count[e] = 0;
-  for (int r = tid; r < p.R; r += kGemvThreads) {
-    const int e = p.idx[r];
-    const bool good = unsigned(e) < unsigned(p.E);
-    S.id[r] = good ? e : -1;
-    if (!good && p.status && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
+    tma_prefetch_desc(&p.tmT);
   }
   if (tid < 8) S.xrow[tid] = -2;
   if (tid == 0) S.abort = 0;
-  __syncthreads();
-  if (warp == 0) {
-    // rank of each row among the rows of its expert, in row order
-    for (int r0 = 0; r0 < p.R; r0 += 32) {
-      const int r = r0 + lane;
-      const int e = r < p.R ? S.id[r] : -1;
-      const uint32_t same = __match_any_sync(0xffffffffu, e);
-      int rank = 0;
-      if (e >= 0) rank = S.count[e] + __popc(same & ((1u << lane) - 1u));
-      __syncwarp();
-      if (e >= 0 && (same >> lane) == 1u) S.count[e] = rank + 1;  // the highest lane
-      if (r < p.R) S.pass_n[r] = rank;
-      __syncwarp();
-    }
-    // first sorted position and first pass of each expert
-    int rows[8], base = 0, pbase = 0;
-    const int per = MOE_MAX_EXPERTS / 32;
-    int nr = 0, np = 0;
-#pragma unroll
-    for (int i = 0; i < per; ++i) {
-      rows[i] = S.count[lane * per + i];
-      nr += rows[i];
-      np += (rows[i] + p.rp - 1) / p.rp;
-    }
-    int sr = nr, sp = np;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int a = __shfl_up_sync(0xffffffffu, sr, d), b = __shfl_up_sync(0xffffffffu, sp, d);
-      if (lane >= d) {
-        sr += a;
-        sp += b;
-      }
-    }
-    if (lane == 31) S.passes = sp;
-    base = sr - nr;
-    pbase = sp - np;
-#pragma unroll
-    for (int i = 0; i < per; ++i) S.first[lane * per + i] = base, base += rows[i];
-    __syncwarp();
-    for (int r = lane; r < p.R; r += 32) {
-      const int e = S.id[r];
-      if (e >= 0) S.sorted[S.first[e] + S.pass_n[r]] = r;
-    }
-    __syncwarp();
-    base = sr - nr;
-#pragma unroll
-    for (int i = 0; i < per; ++i) {
-      for (int a = 0; a < rows[i]; a += p.rp, ++pbase) {
-        S.pass_e[pbase] = lane * per + i;
-        S.pass_at[pbase] = base + a;
-        S.pass_n[pbase] = min(p.rp, rows[i] - a);
-      }
-      base += rows[i];
-    }
+  pdl_wait();
+  pdl_trigger();
+  // ---- passes: routed rows grouped by expert, at most rp rows each
+  if (p.R <= 32) {
+    if (warp == 0) group_few_rows(p, S);
+  } else {
+    for (int e = tid; e < MOE_MAX_EXPERTS; e += kGemvThreads) S.count[e] = 0;
+    for (int r = tid; r < p.R; r += kGemvThreads) S.id[r] = expert_of(p, r);
+    __syncthreads();
+    if (warp == 0) group_rows(p, S);
   }
+  __syncthreads();
   // rows without an expert get zeros
   for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
     if (S.id[r] >= 0) continue;
     uint16_t* y = static_cast<uint16_t*>(p.y) + r * p.ldy;
     for (int n = tid; n < p.N; n += kGemvThreads) y[n] = 0;
   }
-  __syncthreads();
 
   const int blocks = (p.N + kUnitRows - 1) / kUnitRows;
   const long long units = (long long)(S.passes) * blocks;
@@ -270,42 +309,48 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
 
   if (warp == kConsumers / 32) {
     // ------------------------------------------------------------ producer
+    // One lane issues a unit's two or three copies (with a box per 128-byte
+    // span, spread over the lanes, their issue alone took 0.8 us a unit).
     const uint32_t ring_u32 = smem_u32(ring);
-    const int nbox = (p.K / 2 + 127) / 128;
+    const int spans = p.K / 256;
+    const bool rest = p.K % 256 != 0;
+    const uint32_t wbytes = (spans + rest) * 2048;
     const int row_bytes = p.K / 16;
-    int stage = 0;
+    const long long whole = p.scale_bytes & ~15LL;
+    int stage = 0, pass = u0 / blocks, block = u0 - pass * blocks;
     uint32_t phase = 0;
     for (int u = u0; u < u1; ++u) {
-      const int pass = u / blocks;
-      const long long row = (long long)(S.pass_e[pass]) * p.N + (u - pass * blocks) * kUnitRows;
+      const long long row = (long long)(S.pass_e[pass]) * p.N + block * kUnitRows;
+      if (++block == blocks) {
+        block = 0;
+        ++pass;
+      }
       if (!wait_for(p, &empty[stage], phase ^ 1u, &S.abort)) {
         const long long t0 = clock64();  // let the copies in flight land
         while (clock64() - t0 < 4000000) {
         }
         break;
       }
-      const uint32_t st = ring_u32 + stage * p.stage_bytes;
       // the scales of 16 rows are contiguous: the 16-byte blocks that hold them
       const long long a = row * row_bytes;
       const long long end = min(a + (long long)(kUnitRows)*row_bytes, p.scale_bytes);
       const long long a16 = a & ~15LL;
-      const long long whole = p.scale_bytes & ~15LL;
       long long b16 = (end + 15) & ~15LL;
-      if (b16 > p.scale_bytes) b16 = whole;  // the tensor's last bytes: plain loads
-      const uint32_t sbytes = b16 > a16 ? uint32_t(b16 - a16) : 0u;
-      if (end > b16) {
-        const long long from = b16 > a16 ? b16 : a16;
-        if (from + lane < end)
-          ring[stage * p.stage_bytes + scale_at + (from - a16) + lane] = p.scale[from + lane];
+      if (b16 > whole) {  // the tensor's last bytes, fewer than 16: plain loads
+        b16 = whole;
+        if (b16 + lane < end)
+          ring[stage * p.stage_bytes + scale_at + (b16 - a16) + lane] = p.scale[b16 + lane];
         __syncwarp();
       }
       if (lane == 0) {
-        mbar_arrive_expect_tx(&full[stage], nbox * 2048 + sbytes);
+        const uint32_t st = ring_u32 + stage * p.stage_bytes;
+        const uint32_t bar = smem_u32(&full[stage]);
+        const uint32_t sbytes = uint32_t(b16 - a16);
+        mbar_arrive_expect_tx(&full[stage], wbytes + sbytes);
+        if (spans) tma_load_3d<1>(st, &p.tmW, bar, 0, int32_t(row), 0);
+        if (rest) tma_load_3d<1>(st + spans * 2048, &p.tmT, bar, spans * 128, int32_t(row), 0);
         if (sbytes) bulk_load(st + scale_at, p.scale + a16, sbytes, &full[stage]);
       }
-      __syncwarp();
-      for (int i = lane; i < nbox; i += 32)
-        tma_load_3d<1>(st + i * 2048, &p.tmW, smem_u32(&full[stage]), i * 128, int32_t(row), 0);
       __syncwarp();
       if (++stage == p.stages) {
         stage = 0;
@@ -322,7 +367,6 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
   // quarter of a warp reads together differ in bit 2, so that the swizzle
   // puts their 16-byte blocks into different banks
   const int prow = (g >> 1) | ((g & 1) << 2);
-  const uint32_t xs_u32 = smem_u32(xs);
   int buf = 0, staged = -1;
   for (int ub = u0; ub < u1;) {
     const int pass = ub / blocks;
@@ -385,32 +429,41 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
       const uint32_t parity = (at / p.stages) & 1;
       const int n0 = (u - pass * blocks) * kUnitRows;
       const long long row = (long long)(e)*p.N + n0;
-      const uint32_t st = smem_u32(ring) + stage * p.stage_bytes;
-      const uint32_t sc = st + scale_at + uint32_t((row * (p.K / 16)) & 15);
+      const uint8_t* st = ring + stage * p.stage_bytes;
+      const uint8_t* sc = st + scale_at + int((row * (p.K / 16)) & 15) + tig * 2;
+      const uint8_t* sca = sc + prow * (p.K / 16);
+      const uint8_t* scb = sc + (prow + 8) * (p.K / 16);
       wait_for(p, &full[stage], parity, &S.abort);
-      float c[2][4] = {};
-      for (int b = gw; b < nkb; b += kGroupWarps) {
-        const uint32_t box = st + (b >> 1) * 2048;
-        const uint32_t ch = ((b & 1) * 4 + tig) ^ (prow & 7);
-        const uint4 wa = lds128(box + prow * 128 + ch * 16);
-        const uint4 wb = lds128(box + (prow + 8) * 128 + ch * 16);
-        const int k0 = b * 128 + tig * 32;
-        uint32_t sa = 0, sb = 0;  // zero scales behind K: the boxes hold zeros there
-        if (k0 < p.K) {
-          uint16_t va, vb;
-          const uint32_t so = sc + k0 / 16;
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(va) : "r"(so + prow * (p.K / 16)));
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(vb) : "r"(so + (prow + 8) * (p.K / 16)));
-          sa = unpack_e4m3(va);
-          sb = unpack_e4m3(vb);
+      auto load = [&](int b) {
+        Block k;
+        const uint8_t* box = st + (b >> 1) * 2048 + prow * 128 + (((b & 1) * 4 + tig) ^ prow) * 16;
+        k.wa = *reinterpret_cast<const uint4*>(box);
+        k.wb = *reinterpret_cast<const uint4*>(box + 1024);
+        k.sa = k.sb = 0;  // zero scales behind K: the boxes hold zeros there
+        if (b * 128 + tig * 32 < p.K) {
+          k.sa = unpack_e4m3(*reinterpret_cast<const uint16_t*>(sca + b * 8));
+          k.sb = unpack_e4m3(*reinterpret_cast<const uint16_t*>(scb + b * 8));
         }
-        const uint32_t a_w[4] = {wa.x, wa.y, wa.z, wa.w}, b_w[4] = {wb.x, wb.y, wb.z, wb.w};
+        return k;
+      };
+      float c[2][4] = {};
+      Block next = {};
+      if (gw < nkb) next = load(gw);
+      for (int b = gw; b < nkb; b += kGroupWarps) {
+        const Block k = next;
+        if (b + kGroupWarps < nkb) next = load(b + kGroupWarps);
+        const uint32_t a_w[4] = {k.wa.x, k.wa.y, k.wa.z, k.wa.w};
+        const uint32_t b_w[4] = {k.wb.x, k.wb.y, k.wb.z, k.wb.w};
+        const uint8_t* xb = xs + b * xblock + lane * 16;
+        uint4 x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          x[j] = g < p.rp ? *reinterpret_cast<const uint4*>(xb + j * (p.rp * 64))
+                          : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (g < p.rp) x = lds128(xs_u32 + b * xblock + j * (p.rp * 64) + lane * 16);
-          const uint32_t fa = __byte_perm(sa, 0, j < 2 ? 0x1010 : 0x3232);
-          const uint32_t fb = __byte_perm(sb, 0, j < 2 ? 0x1010 : 0x3232);
+          const uint32_t fa = __byte_perm(k.sa, 0, j < 2 ? 0x1010 : 0x3232);
+          const uint32_t fb = __byte_perm(k.sb, 0, j < 2 ? 0x1010 : 0x3232);
           uint32_t ha[4], hb[4];
           unpack_e2m1(a_w[j], ha);
           unpack_e2m1(b_w[j], hb);
@@ -419,8 +472,8 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
             ha[i] = mul_f16x2(ha[i], fa);
             hb[i] = mul_f16x2(hb[i], fb);
           }
-          mma_16816(c[0], ha[0], hb[0], ha[1], hb[1], x.x, x.y);
-          mma_16816(c[1], ha[2], hb[2], ha[3], hb[3], x.z, x.w);
+          mma_16816(c[0], ha[0], hb[0], ha[1], hb[1], x[j].x, x[j].y);
+          mma_16816(c[1], ha[2], hb[2], ha[3], hb[3], x[j].z, x[j].w);
         }
       }
       __syncwarp();
@@ -465,8 +518,19 @@ cudaError_t launch_gemv(const GemvArgs& a, int dev, int grid, int smem, cudaStre
     if (e != cudaSuccess) return e;
     ready[dev].store(true, std::memory_order_release);
   }
-  nvfp4_gemv_kernel<BF16><<<grid, kGemvThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  // a programmatic dependent launch: the set-up up to pdl_wait overlaps the
+  // kernel before
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(kGemvThreads);
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, nvfp4_gemv_kernel<BF16>, a);
 }
 
 // Static shared memory of the kernel, rounded up.
@@ -507,8 +571,9 @@ extern "C" moe_status moe_nvfp4_gemv(const void* x, int64_t ldx, int32_t x_per_s
   GemvArgs a = {};
   const int K = in_features, N = out_features;
   const uint64_t rows = uint64_t(num_experts) * N;
-  if (!make_map_3d(&a.tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, K / 2, rows, 1, K / 2, K / 2,
-                   kUnitRows))
+  if (!make_map_3d(&a.tmT, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, K / 2, rows, 1, K / 2, K / 2,
+                   kUnitRows) ||
+      (K >= 256 && !make_map_spans(&a.tmW, w, rows, K / 2, K / 256, kUnitRows)))
     return MOE_ERR_CUDA;
   a.x = x;
   a.ldx = ldx;
