@@ -345,13 +345,16 @@ MOE_API moe_status moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const vo
  *      row of an id outside [0, num_experts) becomes zero.
  *   w  [E, N, K / 2]: two E2M1 codes (sign, two exponent bits, one mantissa
  *      bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6) a byte, the even k in the low nibble.
- *   w_scale [E, N, K / 16] E4M3, one per 16 inputs; w_scale2 [E] float32.
+ *   w_scale [E, N, K / 16] unsigned E4M3 (the sign bit is ignored), one per 16
+ *      inputs; w_scale2 [E] float32.
  *   y  [num_tokens * k, N] of x's type, ldy elements apart.
  *   activation: MOE_ACT_NONE or MOE_ACT_RELU2.
  *   status: optional device int32, OR-ed into (the caller zeroes it): bit 2
  *      for an id outside [0, num_experts), bit 1 if a wait timed out.
- * Weights times scales are exact on the tensor cores, sums are float32, the
- * result is rounded once.  The weights are read once per 8 rows of an expert.
+ * Weights and scales are exact, an element of x counts to 2^-22 of its row's
+ * largest, sums are float32 and the result is rounded once.  Infinities and
+ * NaN behave as in the formula (a row that holds one takes a slow path).
+ * The weights are read once per 8 rows of an expert (4 in small batches).
  *
  * The call keeps no state and uses no workspace: it allocates nothing, may be
  * captured in a CUDA graph and may overlap in time with others.  y must not

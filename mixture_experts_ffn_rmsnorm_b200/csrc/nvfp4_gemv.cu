@@ -5,26 +5,35 @@
 //   y[t, j, n] = act(s2[e] * sum_k E2M1(w[e, n, k]) * E4M3(s[e, n, k / 16]) * x[t(, j), k]),
 //   e = idx[t, j].
 //
-// Bound: HBM.  A step reads the chosen experts' 9/16 byte per weight once and
-// little else; at 4 bits the arithmetic is the next limit (an SM gets about
-// 40 weights a cycle at the full bandwidth), so the multiply-adds run as
-// mma.sync m16n8k16 (16 weight rows x up to 8 tokens) on f16 operands that
-// are exact: E2M1 times E4M3 has at most 6 significant bits and lies in
-// [2^-10, 2688]; an FP16 token is one already, and a BF16 token row becomes
-// one under a power-of-two scale of its own that puts its largest magnitude
-// in [2^14, 2^15): every element above 2^-29 of the largest keeps all its
-// bits, and what a smaller one loses is at most 2^-39 of the largest, far
-// below the float32 sum's own rounding.  tcgen05 would need the
-// unpacked weights in shared memory, written and read once more per product.
+// Bound: HBM; a step reads the chosen experts' 9/16 byte per weight once and
+// little else.  Unpacking 4-bit weights on the CUDA cores costs more than the
+// stream (conversion, scale and mma.sync take about 230 instructions per 2048
+// weights: 38 us where the bytes take 17.6, 8 tokens over 39 experts), so the
+// block-scaled tensor cores (tcgen05.mma kind::mxf4nvf4, scale vectors of 16)
+// take the weights and their scales as they are stored.  Their other operand
+// is E2M1 too, and a token row becomes one exactly enough in digits: with a
+// power of two of its own, 2^s, a row's elements are whole numbers
+// X = round(2^s x) of magnitude at most 2^22 (the largest at least 2^21), and
+// X = sum_i d_i 8^i with eight digits d_i in -4..3, each an E2M1 value
+// (in halves).  Row n of the other operand is digit n % 8 of token n / 8;
+// eight accumulator columns join as sum_i 8^i acc_i.  An element is off by at
+// most 2^-22 of its row's largest, below what the 16-bit result shows.
+// Infinities and NaN have no digits: they count as zero there and are added
+// in the epilogue from the stored weights.
 //
-// Layout: routed rows with the same expert share a pass of up to 8 rows over
-// its matrix.  All passes' blocks of 16 weight rows ("units") form one list,
-// cut into contiguous ranges, one per CTA, so each CTA streams one contiguous
-// piece of at most a few matrices.  One warp loads units into a ring of
-// shared-memory stages (TMA boxes of 128 bytes x 16 rows, the scales as one
-// bulk copy); four groups of four warps each take a unit, split its K by
-// blocks of 128 over their warps and add up their four partial results in a
-// fixed order.  Results do not depend on the grid.
+// Layout: routed rows of one expert share passes of up to `rp` rows over its
+// matrix.  All passes' blocks of 64 weight rows ("units") form one list, cut
+// into contiguous ranges, one per CTA; a CTA takes two neighbouring units of a
+// pass as one tile of 128 rows (the MMA's M) where it can.
+//   warp 0     TMA: 256 inputs (128 bytes) of a tile's rows into a ring stage;
+//   warp 1     scales from shared memory into TMEM (tcgen05.cp) and the MMAs;
+//   warps 4-7  epilogue: a lane is a weight row, so the lanes' results are
+//              neighbours in y;
+//   warps 8-11 scales from global memory into the ring, in the order of
+//              tcgen05.cp (rows are K / 16 bytes apart, which no tensor map
+//              takes);
+//   warps 4-11 the token rows' digits, at the start of each pass.
+// Results do not depend on the grid.
 #include <cuda_fp16.h>
 
 #include "handle_free.h"
@@ -33,34 +42,42 @@
 namespace moe {
 namespace {
 
-constexpr int kGroups = 4;        // consumer groups
-constexpr int kGroupWarps = 4;    // warps of a group
-constexpr int kConsumers = kGroups * kGroupWarps * 32;
-constexpr int kGemvThreads = kConsumers + 32;
-constexpr int kUnitRows = 16;
-constexpr int kMaxStages = 12;
+constexpr int kGemvThreads = 384;
+constexpr int kUnitRows = 64;
+constexpr int kDigits = 8;
+constexpr int kMaxPassRows = 8;
+constexpr int kStageK = 256;         // inputs of a stage: 128 bytes a row
+constexpr int kStageA = 128 * 128;   // a stage's weights
+constexpr int kStageSf = 4 * 512;    // and their scales: a 512-byte block per 64 inputs
+constexpr int kStageBytes = kStageA + kStageSf;
+constexpr int kMaxStages = 11;
 constexpr int kMaxRows = MOE_NVFP4_MAX_ROWS;
 constexpr int kGemvSmemMax = 232448;
+// TMEM columns: two accumulators, the tokens' scales (ones), the stages' scales
+constexpr uint32_t kColSfb = 2 * kMaxPassRows * kDigits;
+constexpr uint32_t kColSfa = kColSfb + 4;
+constexpr uint32_t kTmemCols = 512;
+static_assert(kColSfa + kMaxStages * 16 <= kTmemCols, "");
+constexpr int kConverters = 8 * 32;  // threads that write digits (warps 4-11)
 
 struct GemvArgs {
-  CUtensorMap tmW;  // [E * N, K / 2] bytes in spans of 128: a box is the whole spans of 16 rows
-  CUtensorMap tmT;  // the same as rows: a box is 128 bytes of 16 rows (the part of a span at the end)
+  CUtensorMap tmW;  // [E * N, K / 2] bytes, boxes of 128 bytes x 64 rows
   const void* x;
   long long ldx;
   int per_slot;
   const int* idx;
   int R, top_k;
   const uint8_t* scale;
-  long long scale_bytes;  // E * N * K / 16
   const float* scale2;
+  const uint8_t* w;
   int E, K, N;
   int relu2;
   void* y;
   long long ldy;
   int* status;
-  int rp;           // rows of a pass, at most (1, 2, 4 or 8)
+  int rp;      // rows of a pass, at most (1, 2, 4 or 8)
+  int xrows;   // digit rows kept in shared memory: max(rp * 8, 16)
   int stages;
-  int stage_bytes;  // multiple of 1024
 };
 
 static_assert(kMaxRows <= 32767 && MOE_MAX_EXPERTS <= 256, "int16 / uint8 tables");
@@ -73,53 +90,14 @@ struct Setup {
   int count[MOE_MAX_EXPERTS];
   int first[MOE_MAX_EXPERTS];
   int passes;
-  int xrow[8];    // token rows staged (-1: zeros)
-  float xinv[8];  // 2^-s of each staged row
-  int changed;    // the last pass whose token rows differ from the staged ones
+  int xrow[kMaxPassRows];    // token rows staged (-1: none)
+  int shift[kMaxPassRows];   // s of each staged row
+  int odd[kMaxPassRows];     // the row holds an infinity or a NaN
+  float amax[kMaxPassRows][8];
+  int bad[kMaxPassRows][8];
+  int changed;  // the last pass whose token rows differ from the staged ones
   volatile int abort;
 };
-
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Eight E2M1 values of a word (low nibble first) as four f16 pairs.
-__device__ __forceinline__ void unpack_e2m1(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}\n"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-
-// Two E4M3 values as an f16 pair (exact; NaN stays NaN).
-__device__ __forceinline__ uint32_t unpack_e4m3(uint16_t v) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(v));
-  return h;
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
 
 // Bounded wait.  Once one has run out, every wait of the CTA returns at once:
 // the warps go on through their barriers and store nothing.
@@ -131,31 +109,34 @@ __device__ __forceinline__ bool wait_for(const GemvArgs& p, uint64_t* bar, uint3
   return false;
 }
 
-// Largest finite magnitude of 8 BF16 values.
-__device__ __forceinline__ float amax8(const uint4& u) {
-  float m = 0.f;
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float lo = fabsf(__uint_as_float(w[i] << 16));
-    const float hi = fabsf(__uint_as_float(w[i] & 0xFFFF0000u));
-    if (lo <= 3.4028235e38f) m = fmaxf(m, lo);
-    if (hi <= 3.4028235e38f) m = fmaxf(m, hi);
-  }
-  return m;
+// D[tmem] (+)= A * SFA x (B * SFB)^T: E2M1 operands, one E4M3 scale per 16.
+__device__ __forceinline__ void umma_nvfp4(uint32_t d, uint64_t adesc, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n\t}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
 }
 
-// 8 BF16 values times a power of two, as f16.
-__device__ __forceinline__ uint4 scaled_f16(const uint4& u, float s) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16) * s,
-                                        __uint_as_float(w[i] & 0xFFFF0000u) * s);
-    o[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+// Block-scaled instruction descriptor: E2M1 x E2M1, K-major, unsigned E4M3
+// scales (bit 23 clear), scale ids 0, M = 128.
+__device__ __forceinline__ uint32_t nvfp4_idesc(uint32_t N) {
+  return (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// 32 rows of 16 bytes (512 contiguous bytes of shared memory) to 4 TMEM
+// columns of lanes 0-31, and the same to the other three lane quarters.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t smem) {
+  uint64_t d = 0;
+  d |= uint64_t((smem >> 4) & 0x3FFFu);
+  d |= uint64_t(128 >> 4) << 16;
+  d |= uint64_t(128 >> 4) << 32;  // eight rows are 128 bytes
+  d |= uint64_t(1) << 46;         // version; no swizzle
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 
 __device__ __forceinline__ int expert_of(const GemvArgs& p, int r) {
@@ -249,40 +230,159 @@ __device__ __forceinline__ void group_rows(const GemvArgs& p, Setup& S) {
   }
 }
 
-// The operands of one 128-wide block that a lane takes from a stage: 32
-// weights of two rows and their two scales each, as f16 pairs.
-struct Block {
-  uint4 wa, wb;
-  uint32_t sa, sb;
-};
+// Eight elements of a token row in float32.
+template <bool BF16>
+__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BF16) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.4028235e38f; }
+
+__device__ __forceinline__ float pow2(int e) {  // e in -126..127
+  return __uint_as_float(uint32_t(e + 127) << 23);
+}
+
+// The E2M1 codes of the eight balanced base-8 digits of X (|X| <= 2^22), digit
+// i in nibble i.  With U = X + 4 (1 + 8 + ... + 8^7), digit i is
+// ((U >> 3 i) & 7) - 4.
+__device__ __forceinline__ uint32_t digit_codes(int X) {
+  uint32_t t = uint32_t(X + 9586980);
+  // 3-bit fields to nibbles
+  t = (t & 0x00000FFFu) | ((t & 0x00FFF000u) << 4);
+  t = (t & 0x003F003Fu) | ((t & 0x0FC00FC0u) << 2);
+  t = (t & 0x07070707u) | ((t & 0x38383838u) << 1);
+  // t - 4 as sign and magnitude (in halves): 4..7 -> 0..3, 0..3 -> -4..-1
+  const uint32_t s = ~t & 0x44444444u;
+  const uint32_t neg = s >> 2;
+  const uint32_t mag = ((t ^ (neg * 3u)) & 0x33333333u) + neg;
+  return mag | (s << 1);
+}
+
+// 8 x 8 nibbles: w[i] nibble j <-> w[j] nibble i.
+__device__ __forceinline__ void transpose_nibbles(uint32_t (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // halves of 16 bits: rows i, i + 4
+    const uint32_t a = w[i], b = w[i + 4];
+    w[i] = __byte_perm(a, b, 0x5410);
+    w[i + 4] = __byte_perm(a, b, 0x7632);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if ((i & 2) == 0) {  // bytes: rows i, i + 2
+      const uint32_t a = w[i], b = w[i + 2];
+      w[i] = __byte_perm(a, b, 0x6240);
+      w[i + 2] = __byte_perm(a, b, 0x7351);
+    }
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {  // nibbles: rows i, i + 1
+    const uint32_t a = w[i], b = w[i + 1];
+    w[i] = (a & 0x0F0F0F0Fu) | ((b & 0x0F0F0F0Fu) << 4);
+    w[i + 1] = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
+  }
+}
+
+// 16 scale bytes of one weight row from byte `at` on, zeros from `n` valid
+// ones on; `align` is the largest power of two (2..16) that divides every
+// row's address.
+__device__ __forceinline__ uint4 load_scales(const uint8_t* p, int n, int align) {
+  uint4 u = make_uint4(0, 0, 0, 0);
+  if (n >= 16 && align == 16) return *reinterpret_cast<const uint4*>(p);
+  if (align >= 8) {
+    if (n >= 8) {
+      const uint2 a = *reinterpret_cast<const uint2*>(p);
+      u.x = a.x, u.y = a.y;
+    }
+    if (n >= 16) {
+      const uint2 a = *reinterpret_cast<const uint2*>(p + 8);
+      u.z = a.x, u.w = a.y;
+    }
+    if ((n & 7) == 0) return u;
+  } else if (align == 4) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
+    if (n >= 4) u.x = q[0];
+    if (n >= 8) u.y = q[1];
+    if (n >= 12) u.z = q[2];
+    if (n >= 16) u.w = q[3];
+    if ((n & 3) == 0) return u;
+  }
+  const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = 2 * i < n ? q[i] : 0;
+  return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+}
+
+// What the infinities and NaN of a token row add to weight row `row`.
+template <bool BF16>
+__device__ __noinline__ float odd_part(const GemvArgs& p, const uint16_t* x, long long row) {
+  float sum = 0.f;
+  for (int k = 0; k < p.K; ++k) {
+    const uint32_t b = x[k];
+    const float v = BF16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half(uint16_t(b)));
+    if (finite(v)) continue;
+    const uint32_t code = (p.w[row * (p.K / 2) + k / 2] >> (4 * (k & 1))) & 15;
+    const uint32_t m = code & 7;
+    const float mag = m < 2 ? 0.5f * m : (1.f + 0.5f * (m & 1)) * pow2(int(m >> 1) - 1);
+    const uint32_t e4 = p.scale[row * (p.K / 16) + k / 16];
+    const float sc = (e4 & 0x78) ? (1.f + (e4 & 7) / 8.f) * pow2(int(e4 >> 3 & 15) - 7)
+                                 : (e4 & 7) * pow2(-9);
+    sum += v * ((code & 8) ? -mag : mag) * sc;
+  }
+  return sum;
+}
 
 template <bool BF16>
 __global__ void __launch_bounds__(kGemvThreads, 1)
     nvfp4_gemv_kernel(const __grid_constant__ GemvArgs p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Setup S;
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
-  __shared__ float part[kGroups][2][kGroupWarps][8 * kUnitRows];
-  __shared__ float s_amax[8][2];
+  __shared__ uint64_t full[kMaxStages], sf_full[kMaxStages], empty[kMaxStages];
+  __shared__ uint64_t tfull[2], tempty[2], xfull, drain;
+  __shared__ uint32_t tmem_slot;
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
-  uint8_t* ring = smem_raw + pad;
-  const int nkb = (p.K + 127) / 128;
-  const int xblock = p.rp * 256;  // bytes of a 128-wide block of the staged token rows
-  const int scale_at = (p.K / 2 + 127) / 128 * 2048;  // scales behind a stage's boxes
-  uint8_t* xs = ring + p.stages * p.stage_bytes;
+  uint8_t* ring = smem_raw + pad;                 // stages: weights, then all stages' scales
+  uint8_t* sf = ring + p.stages * kStageA;
+  uint8_t* xs = sf + p.stages * kStageSf;         // the digits
+  const int nst = (p.K + kStageK - 1) / kStageK;  // stages of a tile
+  const int xblock = p.xrows * 128;               // digit rows of one stage's inputs
+  uint8_t* ones = xs + nst * xblock;              // 512 bytes: the tokens' scales
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kGroupWarps);
+      mbar_init(&sf_full[s], 4);
+      mbar_init(&empty[s], 1);
     }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 4);
+    }
+    mbar_init(&xfull, 1);
+    mbar_init(&drain, 1);
     fence_barrier_init();
     tma_prefetch_desc(&p.tmW);
-    tma_prefetch_desc(&p.tmT);
+    S.abort = 0;
   }
-  if (tid < 8) S.xrow[tid] = -2;
-  if (tid == 0) S.abort = 0;
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  if (tid >= 128 && tid < 256) reinterpret_cast<uint32_t*>(ones)[tid - 128] = 0x38383838u;
+  if (tid < kMaxPassRows) S.xrow[tid] = -2;
+  fence_proxy_async_smem();
   pdl_wait();
   pdl_trigger();
   // ---- passes: routed rows grouped by expert, at most rp rows each
@@ -290,11 +390,14 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     if (warp == 0) group_few_rows(p, S);
   } else {
     for (int e = tid; e < MOE_MAX_EXPERTS; e += kGemvThreads) S.count[e] = 0;
-    for (int r = tid; r < p.R; r += kGemvThreads) S.id[r] = expert_of(p, r);
+    for (int r = tid; r < p.R; r += kGemvThreads) S.id[r] = int16_t(expert_of(p, r));
     __syncthreads();
     if (warp == 0) group_rows(p, S);
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
   // rows without an expert get zeros
   for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
     if (S.id[r] >= 0) continue;
@@ -307,214 +410,266 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
   const int u0 = int(units * blockIdx.x / gridDim.x);
   const int u1 = int(units * (blockIdx.x + 1) / gridDim.x);
 
-  if (warp == kConsumers / 32) {
+  // Every role walks the same tiles: u -> pass, first unit inside the pass,
+  // two units where this CTA has both of a pass.
+  if (warp == 0) {
     // ------------------------------------------------------------ producer
-    // One lane issues a unit's two or three copies (with a box per 128-byte
-    // span, spread over the lanes, their issue alone took 0.8 us a unit).
-    const uint32_t ring_u32 = smem_u32(ring);
-    const int spans = p.K / 256;
-    const bool rest = p.K % 256 != 0;
-    const uint32_t wbytes = (spans + rest) * 2048;
-    const int row_bytes = p.K / 16;
-    const long long whole = p.scale_bytes & ~15LL;
-    int stage = 0, pass = u0 / blocks, block = u0 - pass * blocks;
-    uint32_t phase = 0;
-    for (int u = u0; u < u1; ++u) {
-      const long long row = (long long)(S.pass_e[pass]) * p.N + block * kUnitRows;
-      if (++block == blocks) {
-        block = 0;
-        ++pass;
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = u0, two; u < u1 && ok; u += two) {
+        const int pass = u / blocks, block = u - pass * blocks;
+        two = u + 1 < u1 && block + 1 < blocks ? 2 : 1;
+        const int row = S.pass_e[pass] * p.N + block * kUnitRows;
+        for (int k = 0; k < nst; ++k) {
+          if (!wait_for(p, &empty[stage], phase ^ 1u, &S.abort)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[stage], two * 8192);
+          for (int h = 0; h < two; ++h)
+            tma_load_3d<1>(smem_u32(ring + stage * kStageA + h * 8192), &p.tmW,
+                           smem_u32(&full[stage]), k * 128, row + h * kUnitRows, 0);
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
       }
-      if (!wait_for(p, &empty[stage], phase ^ 1u, &S.abort)) {
+      if (!ok) {
         const long long t0 = clock64();  // let the copies in flight land
         while (clock64() - t0 < 4000000) {
         }
-        break;
-      }
-      // the scales of 16 rows are contiguous: the 16-byte blocks that hold them
-      const long long a = row * row_bytes;
-      const long long end = min(a + (long long)(kUnitRows)*row_bytes, p.scale_bytes);
-      const long long a16 = a & ~15LL;
-      long long b16 = (end + 15) & ~15LL;
-      if (b16 > whole) {  // the tensor's last bytes, fewer than 16: plain loads
-        b16 = whole;
-        if (b16 + lane < end)
-          ring[stage * p.stage_bytes + scale_at + (b16 - a16) + lane] = p.scale[b16 + lane];
-        __syncwarp();
-      }
-      if (lane == 0) {
-        const uint32_t st = ring_u32 + stage * p.stage_bytes;
-        const uint32_t bar = smem_u32(&full[stage]);
-        const uint32_t sbytes = uint32_t(b16 - a16);
-        mbar_arrive_expect_tx(&full[stage], wbytes + sbytes);
-        if (spans) tma_load_3d<1>(st, &p.tmW, bar, 0, int32_t(row), 0);
-        if (rest) tma_load_3d<1>(st + spans * 2048, &p.tmT, bar, spans * 128, int32_t(row), 0);
-        if (sbytes) bulk_load(st + scale_at, p.scale + a16, sbytes, &full[stage]);
-      }
-      __syncwarp();
-      if (++stage == p.stages) {
-        stage = 0;
-        phase ^= 1u;
       }
     }
-    return;
-  }
-
-  // -------------------------------------------------------------- consumers
-  const int group = warp / kGroupWarps, gw = warp % kGroupWarps;
-  const int g = lane >> 2, tig = lane & 3;
-  // mma row g is weight row prow (and g + 8 is prow + 8): the two rows that a
-  // quarter of a warp reads together differ in bit 2, so that the swizzle
-  // puts their 16-byte blocks into different banks
-  const int prow = (g >> 1) | ((g & 1) << 2);
-  int buf = 0, staged = -1;
-  for (int ub = u0; ub < u1;) {
-    const int pass = ub / blocks;
-    const int ue = min(u1, (pass + 1) * blocks);  // this CTA's units of the pass
-    const int n_rows = S.pass_n[pass];
-    const int16_t* rows = S.sorted + S.pass_at[pass];
-    const int e = S.pass_e[pass];
-
-    // ---- the pass's token rows as f16 fragments in shared memory
-    {
-      const int n = tid >> 6, i = tid & 63;  // 64 threads a row
-      const int r = n < n_rows ? rows[n] : -1;
-      const int want = n < n_rows ? (p.per_slot ? r : r / p.top_k) : -1;
-      named_barrier(1, kConsumers);  // the pass before is done with xs
-      if (i == 0 && S.xrow[n] != want) S.changed = pass;
-      named_barrier(1, kConsumers);
-      if (staged < 0 || S.changed == pass) {
-        const uint16_t* xr = static_cast<const uint16_t*>(p.x) + (want < 0 ? 0 : want) * p.ldx;
-        float s = 1.f;
-        if constexpr (BF16) {
-          float m = 0.f;
-          if (want >= 0)
-            for (int k = i * 8; k < p.K; k += 512)
-              m = fmaxf(m, amax8(*reinterpret_cast<const uint4*>(xr + k)));
-#pragma unroll
-          for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-          if (lane == 0) s_amax[n][(tid >> 5) & 1] = m;
-          named_barrier(1, kConsumers);
-          m = fmaxf(s_amax[n][0], s_amax[n][1]);
-          // m in [2^ex, 2^(ex + 1)): s = 2^(14 - ex), at most 2^126
-          const int ex = m > 0.f ? max(int(__float_as_uint(m) >> 23), 1) - 127 : 14;
-          const int sh = min(14 - ex, 126);
-          s = __uint_as_float(uint32_t(sh + 127) << 23);
-          if (i == 0) S.xinv[n] = __uint_as_float(uint32_t(127 - sh) << 23);
-        } else if (i == 0) {
-          S.xinv[n] = 1.f;
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      tmem_cp_scales(tmem + kColSfb, smem_u32(ones));
+      int stage = 0, it = 0, seen = -1;
+      uint32_t phase = 0, xphase = 0;
+      bool ok = true;
+      for (int u = u0, two; u < u1 && ok; u += two) {
+        const int pass = u / blocks, block = u - pass * blocks;
+        two = u + 1 < u1 && block + 1 < blocks ? 2 : 1;
+        if (pass != seen) {
+          if (!wait_for(p, &xfull, xphase, &S.abort)) break;
+          xphase ^= 1u;
+          seen = pass;
         }
-        if (i == 0) S.xrow[n] = want;
-        if (n < p.rp) {
-          // chunk c = 8 elements: block c / 16, lane n * 4 + (c / 4) % 4, quarter c % 4
-          for (int c = i; c < nkb * 16; c += 64) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (want >= 0 && c * 8 < p.K) {
-              v = *reinterpret_cast<const uint4*>(xr + c * 8);
-              if constexpr (BF16) v = scaled_f16(v, s);
+        const int cols = max(16, (S.pass_n[pass] * kDigits + 15) & ~15);
+        const uint32_t idesc = nvfp4_idesc(cols);
+        const uint32_t d = tmem + uint32_t((it & 1) * kMaxPassRows * kDigits);
+        if (!wait_for(p, &tempty[it & 1], ((it >> 1) & 1) ^ 1u, &S.abort)) break;
+        tc_fence_after();
+        for (int k = 0; k < nst; ++k) {
+          if (!wait_for(p, &full[stage], phase, &S.abort) ||
+              !wait_for(p, &sf_full[stage], phase, &S.abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sfa = tmem + kColSfa + stage * 16;
+          const int steps = min(4, (p.K - k * kStageK + 63) / 64);
+          for (int j = 0; j < steps; ++j)
+            tmem_cp_scales(sfa + j * 4, smem_u32(sf + stage * kStageSf + j * 512));
+          const uint64_t ad = smem_desc_sw128(ring + stage * kStageA);
+          const uint64_t bd = smem_desc_sw128(xs + k * xblock);
+          for (int j = 0; j < steps; ++j)
+            umma_nvfp4(d, ad + j * 2, bd + j * 2, idesc, sfa + j * 4, tmem + kColSfb,
+                       (k | j) ? 1u : 0u);
+          umma_commit(&empty[stage]);
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok) umma_commit(&tfull[it & 1]);
+        ++it;
+      }
+      umma_commit(&drain);
+      int zero = 0;
+      mbar_wait(&drain, 0, &zero);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------- digits, then epilogue or scales
+    const int cw = warp - 4;
+    int stage = 0, it = 0;
+    uint32_t phase = 0;
+    const int row_bytes = p.K / 16;
+    const int align = min(16, row_bytes & -row_bytes);
+    for (int ub = u0; ub < u1;) {
+      const int pass = ub / blocks;
+      const int ue = min(u1, (pass + 1) * blocks);  // this CTA's units of the pass
+      const int n_rows = S.pass_n[pass], e = S.pass_e[pass];
+      const int16_t* rows = S.sorted + S.pass_at[pass];
+      {
+        // a row's 256-wide blocks over 8, 4, 2 or 1 warps
+        const int per = n_rows > 4 ? 1 : n_rows > 2 ? 2 : n_rows > 1 ? 4 : 8;
+        const int n = cw / per, part = cw % per;
+        const int want = n < n_rows ? (p.per_slot ? rows[n] : rows[n] / p.top_k) : -1;
+        // the pass before is done: its epilogues are, so its MMAs are
+        named_barrier(1, kConverters);
+        if (lane == 0 && part == 0 && want >= 0 && S.xrow[n] != want) S.changed = pass;
+        named_barrier(1, kConverters);
+        if (S.changed == pass) {
+          const uint16_t* xr = static_cast<const uint16_t*>(p.x) + (want < 0 ? 0 : want) * p.ldx;
+          if (want >= 0) {
+            float m = 0.f;
+            int bad = 0;
+#pragma unroll 2
+            for (int k = part * 256 + lane * 8; k < p.K; k += per * 256) {
+              float v[8];
+              load8<BF16>(xr + k, v);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if (finite(v[i]))
+                  m = fmaxf(m, fabsf(v[i]));
+                else
+                  bad = 1;
+              }
             }
-            *reinterpret_cast<uint4*>(xs + (c >> 4) * xblock + (c & 3) * (p.rp * 64) +
-                                      (n * 4 + ((c >> 2) & 3)) * 16) = v;
+#pragma unroll
+            for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+            bad = __any_sync(0xffffffffu, bad);
+            if (lane == 0) {
+              S.amax[n][part] = m;
+              S.bad[n][part] = bad;
+            }
+          }
+          named_barrier(1, kConverters);
+          if (want >= 0) {
+            float m = 0.f;
+            int bad = 0;
+            for (int i = 0; i < per; ++i) {
+              m = fmaxf(m, S.amax[n][i]);
+              bad |= S.bad[n][i];
+            }
+            // the largest magnitude to [2^21, 2^22); a float32's exponent, or a subnormal's
+            const uint32_t mb = __float_as_uint(m);
+            const int ex = mb >> 23 ? int(mb >> 23) - 127 : -118 - __clz(mb | 1u);
+            const int sh = mb ? 21 - ex : 0;
+            const float f1 = pow2(sh / 2), f2 = pow2(sh - sh / 2);
+            if (lane == 0 && part == 0) {
+              S.xrow[n] = want;
+              S.shift[n] = sh;
+              S.odd[n] = bad;
+            }
+            for (int k = part * 256 + lane * 8; k < nst * kStageK; k += per * 256) {
+              uint32_t w[8] = {};
+              if (k < p.K) {
+                float v[8];
+                load8<BF16>(xr + k, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  w[i] = digit_codes(finite(v[i]) ? __float2int_rn(v[i] * f1 * f2) : 0);
+                transpose_nibbles(w);
+              }
+              // digit i of eight inputs: 4 bytes of row n * 8 + i, swizzled as TMA would
+              uint8_t* dst = xs + (k / kStageK) * xblock + n * kDigits * 128 + (lane & 3) * 4;
+#pragma unroll
+              for (int i = 0; i < kDigits; ++i)
+                *reinterpret_cast<uint32_t*>(dst + i * 128 + ((lane >> 2) ^ i) * 16) = w[i];
+            }
+          }
+          fence_proxy_async_smem();
+          named_barrier(1, kConverters);
+        }
+        if (warp == 4 && lane == 0) mbar_arrive(&xfull);
+      }
+      const float s2 = p.scale2[e];
+      for (int u = ub, two; u < ue; u += two) {
+        two = u + 1 < ue ? 2 : 1;
+        const int n0 = (u - pass * blocks) * kUnitRows;
+        const int valid = min(two * kUnitRows, p.N - n0);  // weight rows of the tile
+        if (warp < 8) {
+          // -------------------------------------------------------- epilogue
+          const int r = cw * 32 + lane;
+          const bool ok = wait_for(p, &tfull[it & 1], (it >> 1) & 1, &S.abort);
+          tc_fence_after();
+          const uint32_t d = tmem + (uint32_t(cw * 32) << 16) +
+                             uint32_t((it & 1) * kMaxPassRows * kDigits);
+          for (int n = 0; n < n_rows && cw * 32 < valid; ++n) {
+            uint32_t acc[1][kDigits];
+            tmem_ld_32x32b_n<kDigits>(d + uint32_t(n * kDigits), acc[0]);
+            tmem_ld_wait_regs(acc);
+            float v = __uint_as_float(acc[0][kDigits - 1]);
+#pragma unroll
+            for (int i = kDigits - 2; i >= 0; --i) v = fmaf(v, 8.f, __uint_as_float(acc[0][i]));
+            // digits count halves: times 2^(1 - s), in whatever range the factors lie
+            const double unscale =
+                __longlong_as_double((long long)(1023 + 1 - S.shift[n]) << 52);
+            v = float(double(v) * unscale * double(s2));
+            if (r < valid && ok && !S.abort) {
+              const long long src = p.per_slot ? rows[n] : rows[n] / p.top_k;
+              if (S.odd[n])
+                v += s2 * odd_part<BF16>(p, static_cast<const uint16_t*>(p.x) + src * p.ldx,
+                                         (long long)(e)*p.N + n0 + r);
+              if (p.relu2) v = v <= 0.f ? 0.f : v * v;  // NaN stays NaN
+              const long long o = rows[n] * p.ldy + n0 + r;
+              if constexpr (BF16)
+                static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
+              else
+                static_cast<__half*>(p.y)[o] = __float2half_rn(v);
+            }
+            __syncwarp();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[it & 1]);
+          ++it;
+        } else {
+          // ---------------------------------------------------------- scales
+          const int r = (cw - 4) * 32 + lane;  // weight row of the tile
+          const uint8_t* src = p.scale + ((long long)(e)*p.N + n0 + r) * row_bytes;
+          auto load = [&](int k) {
+            return r < valid ? load_scales(src + k * 16, min(16, row_bytes - k * 16), align)
+                             : make_uint4(0, 0, 0, 0);
+          };
+          uint4 next = load(0);
+          for (int k = 0; k < nst; ++k) {
+            const uint4 v = next;
+            if (k + 1 < nst) next = load(k + 1);
+            wait_for(p, &empty[stage], phase ^ 1u, &S.abort);
+            // row r of a 64-input block: bytes (r % 32) * 16 + (r / 32) * 4
+            uint32_t* dst =
+                reinterpret_cast<uint32_t*>(sf + stage * kStageSf) + lane * 4 + (cw - 4);
+            dst[0] = v.x & 0x7F7F7F7Fu;  // scales are unsigned
+            dst[128] = v.y & 0x7F7F7F7Fu;
+            dst[256] = v.z & 0x7F7F7F7Fu;
+            dst[384] = v.w & 0x7F7F7F7Fu;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sf_full[stage]);
+            if (++stage == p.stages) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
         }
-        named_barrier(1, kConsumers);
-        staged = pass;
       }
+      ub = ue;
     }
-
-    const float s2 = p.scale2[e];
-    for (int u = ub + ((group - (ub - u0)) & (kGroups - 1)); u < ue; u += kGroups) {
-      const int at = u - u0;
-      const int stage = at % p.stages;
-      const uint32_t parity = (at / p.stages) & 1;
-      const int n0 = (u - pass * blocks) * kUnitRows;
-      const long long row = (long long)(e)*p.N + n0;
-      const uint8_t* st = ring + stage * p.stage_bytes;
-      const uint8_t* sc = st + scale_at + int((row * (p.K / 16)) & 15) + tig * 2;
-      const uint8_t* sca = sc + prow * (p.K / 16);
-      const uint8_t* scb = sc + (prow + 8) * (p.K / 16);
-      wait_for(p, &full[stage], parity, &S.abort);
-      auto load = [&](int b) {
-        Block k;
-        const uint8_t* box = st + (b >> 1) * 2048 + prow * 128 + (((b & 1) * 4 + tig) ^ prow) * 16;
-        k.wa = *reinterpret_cast<const uint4*>(box);
-        k.wb = *reinterpret_cast<const uint4*>(box + 1024);
-        k.sa = k.sb = 0;  // zero scales behind K: the boxes hold zeros there
-        if (b * 128 + tig * 32 < p.K) {
-          k.sa = unpack_e4m3(*reinterpret_cast<const uint16_t*>(sca + b * 8));
-          k.sb = unpack_e4m3(*reinterpret_cast<const uint16_t*>(scb + b * 8));
-        }
-        return k;
-      };
-      float c[2][4] = {};
-      Block next = {};
-      if (gw < nkb) next = load(gw);
-      for (int b = gw; b < nkb; b += kGroupWarps) {
-        const Block k = next;
-        if (b + kGroupWarps < nkb) next = load(b + kGroupWarps);
-        const uint32_t a_w[4] = {k.wa.x, k.wa.y, k.wa.z, k.wa.w};
-        const uint32_t b_w[4] = {k.wb.x, k.wb.y, k.wb.z, k.wb.w};
-        const uint8_t* xb = xs + b * xblock + lane * 16;
-        uint4 x[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          x[j] = g < p.rp ? *reinterpret_cast<const uint4*>(xb + j * (p.rp * 64))
-                          : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t fa = __byte_perm(k.sa, 0, j < 2 ? 0x1010 : 0x3232);
-          const uint32_t fb = __byte_perm(k.sb, 0, j < 2 ? 0x1010 : 0x3232);
-          uint32_t ha[4], hb[4];
-          unpack_e2m1(a_w[j], ha);
-          unpack_e2m1(b_w[j], hb);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            ha[i] = mul_f16x2(ha[i], fa);
-            hb[i] = mul_f16x2(hb[i], fb);
-          }
-          mma_16816(c[0], ha[0], hb[0], ha[1], hb[1], x[j].x, x[j].y);
-          mma_16816(c[1], ha[2], hb[2], ha[3], hb[3], x[j].z, x[j].w);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[stage]);
-      // the four warps' partial sums, [token][weight row]
-      float* mine = part[group][buf][gw];
-      mine[(2 * tig) * kUnitRows + prow] = c[0][0] + c[1][0];
-      mine[(2 * tig + 1) * kUnitRows + prow] = c[0][1] + c[1][1];
-      mine[(2 * tig) * kUnitRows + prow + 8] = c[0][2] + c[1][2];
-      mine[(2 * tig + 1) * kUnitRows + prow + 8] = c[0][3] + c[1][3];
-      named_barrier(2 + group, kGroupWarps * 32);
-      const int t = tid & 127;
-      const int tok = t / kUnitRows, n = n0 + t % kUnitRows;
-      if (tok < n_rows && n < p.N && !S.abort) {
-        float v = part[group][buf][0][t];
-#pragma unroll
-        for (int w = 1; w < kGroupWarps; ++w) v += part[group][buf][w][t];
-        // one rounding to float32, in whatever range the three factors lie
-        v = float(double(v) * double(s2) * double(S.xinv[tok]));
-        if (p.relu2) v = v <= 0.f ? 0.f : v * v;  // NaN stays NaN
-        const long long o = rows[tok] * p.ldy + n;
-        if constexpr (BF16)
-          static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
-        else
-          static_cast<__half*>(p.y)[o] = __float2half_rn(v);
-      }
-      buf ^= 1;
-    }
-    ub = ue;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
   }
 }
+
+// Static shared memory of the kernel, at most.
+constexpr int kGemvStatic = int(sizeof(Setup)) + 512;
 
 template <bool BF16>
 cudaError_t launch_gemv(const GemvArgs& a, int dev, int grid, int smem, cudaStream_t stream) {
   static std::atomic<bool> ready[kMaxDevices];
   if (!ready[dev].load(std::memory_order_acquire)) {
-    cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, nvfp4_gemv_kernel<BF16>);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(nvfp4_gemv_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kGemvSmemMax - int(fa.sharedSizeBytes));
+    const cudaError_t e =
+        cudaFuncSetAttribute(nvfp4_gemv_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kGemvSmemMax - kGemvStatic);
     if (e != cudaSuccess) return e;
     ready[dev].store(true, std::memory_order_release);
   }
@@ -532,10 +687,6 @@ cudaError_t launch_gemv(const GemvArgs& a, int dev, int grid, int smem, cudaStre
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, nvfp4_gemv_kernel<BF16>, a);
 }
-
-// Static shared memory of the kernel, rounded up.
-constexpr int kGemvStatic = int(sizeof(Setup)) + 2 * 8 * kMaxStages +
-                            int(sizeof(float)) * kGroups * 2 * kGroupWarps * 8 * kUnitRows + 256;
 
 }  // namespace
 }  // namespace moe
@@ -571,9 +722,8 @@ extern "C" moe_status moe_nvfp4_gemv(const void* x, int64_t ldx, int32_t x_per_s
   GemvArgs a = {};
   const int K = in_features, N = out_features;
   const uint64_t rows = uint64_t(num_experts) * N;
-  if (!make_map_3d(&a.tmT, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, K / 2, rows, 1, K / 2, K / 2,
-                   kUnitRows) ||
-      (K >= 256 && !make_map_spans(&a.tmW, w, rows, K / 2, K / 256, kUnitRows)))
+  if (!make_map_3d(&a.tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, K / 2, rows, 1, K / 2, K / 2,
+                   kUnitRows))
     return MOE_ERR_CUDA;
   a.x = x;
   a.ldx = ldx;
@@ -582,8 +732,8 @@ extern "C" moe_status moe_nvfp4_gemv(const void* x, int64_t ldx, int32_t x_per_s
   a.R = num_tokens * top_k;
   a.top_k = top_k;
   a.scale = static_cast<const uint8_t*>(w_scale);
-  a.scale_bytes = (long long)(rows) * (K / 16);
   a.scale2 = w_scale2;
+  a.w = static_cast<const uint8_t*>(w);
   a.E = num_experts;
   a.K = K;
   a.N = N;
@@ -591,22 +741,23 @@ extern "C" moe_status moe_nvfp4_gemv(const void* x, int64_t ldx, int32_t x_per_s
   a.y = y;
   a.ldy = ldy;
   a.status = status;
-  // a stage: 16 rows of weights in whole boxes, then their scales (up to 15
-  // bytes more on either side).  Beside the stages lie a pass's token rows:
-  // as many as an expert can have when ids are distinct, at most 8 (the
-  // mma's columns), and fewer where those would leave less than two stages.
-  const int boxes = (K / 2 + 127) / 128;
-  a.stage_bytes = (boxes * 2048 + K + 32 + 1023) / 1024 * 1024;
-  const int nkb = (K + 127) / 128;
-  const int room = kGemvSmemMax - kGemvStatic - 1024 - 1024;
+  // Rows of a pass: as many as an expert can have when ids are distinct, but
+  // at most 4 while the experts see fewer than 4 rows on average (their
+  // digits take shared memory from the ring), else 8, and fewer where the
+  // digits would leave less than four stages.
   a.rp = num_tokens > 4 ? 8 : num_tokens > 2 ? 4 : num_tokens;
-  while (a.rp > 1 && room - nkb * a.rp * 256 < 2 * a.stage_bytes) a.rp /= 2;
-  const int xbytes = nkb * a.rp * 256;
-  a.stages = (room - xbytes) / a.stage_bytes;
+  if (a.rp == 8 && a.R < 4 * num_experts) a.rp = 4;
+  const int nst = (K + kStageK - 1) / kStageK;
+  const int room = kGemvSmemMax - kGemvStatic - 1024 - 512;
+  for (;; a.rp /= 2) {
+    a.xrows = a.rp * kDigits < 16 ? 16 : a.rp * kDigits;
+    a.stages = (room - nst * a.xrows * 128) / kStageBytes;
+    if (a.stages >= 4 || a.rp == 1) break;
+  }
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   const long long most = (long long)(a.R) * ((N + kUnitRows - 1) / kUnitRows);
   const int grid = int(most < sms ? most : sms);
-  const int smem = 1024 + a.stages * a.stage_bytes + xbytes;
+  const int smem = 1024 + a.stages * kStageBytes + nst * a.xrows * 128 + 512;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const cudaError_t err = dtype == MOE_DTYPE_BF16 ? launch_gemv<true>(a, dev, grid, smem, cs)
                                                   : launch_gemv<false>(a, dev, grid, smem, cs);

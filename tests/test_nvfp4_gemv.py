@@ -1,16 +1,17 @@
 """moe_nvfp4_gemv against its definition in 64 bits.
 
-Tolerances.  A weight (E2M1 times E4M3, 6 significant bits at most) and a token
-element (11 bits) multiply exactly in float32.  A float32 sum of K products, in
-any order and with every addition off by at most one unit in the last place
-(2^-23 of the partial sum, truncation allowed), is off by at most
-K * 2^-23 * S, S the sum of the products' magnitudes.  A BF16 row is scaled into
-FP16 by a power of two that puts its largest element at 2^14 or above, so an
-element is off by at most 2^-25 there: 2^-39 of the largest, times the sum of
-the weights' magnitudes.  Scaling the sum to float32 and rounding the result to
-its type add half a step each (2^-24 and eps / 2 of the value, and half the
-smallest subnormal of the type); relu^2 of a value off by d is off by at most
-2 |v| d + d^2.
+Tolerances.  Weights (E2M1 times unsigned E4M3) are exact.  A token element is
+written as a whole number X of units 2^-s with |X| <= 2^22 and its row's largest at
+2^21 or above, so it is off by at most half a unit: 2^-22 of the row's largest, times
+the sum of the weights' magnitudes.  X has digits -4..3 to base 8 whose magnitudes add
+up to at most 3 |X|, and a product of a weight and a digit is exact in float32.  A
+float32 sum of K products, in any order and with every addition off by at most one
+unit in the last place (2^-23 of the partial sum, truncation allowed), is off by at
+most K * 2^-23 of the sum of their magnitudes; joining eight digits' sums adds eight
+such steps: together (K + 8) * 2^-23 * 3 S, S the sum of |w x|.  Scaling the sum to
+float32 and rounding the result to its type add half a step each (2^-24 and eps / 2 of
+the value, and half the smallest subnormal of the type); relu^2 of a value off by d is
+off by at most 2 |v| d + d^2.
 """
 import pytest
 
@@ -28,10 +29,9 @@ BAD_INDEX_BIT = 2
 
 
 def weights(E, N, K, gen):
-    """Codes uniform over all 16, scales over all finite E4M3 values (signs and subnormals among them)."""
+    """Codes uniform over all 16, scales over all finite unsigned E4M3 values (subnormals among them)."""
     w = torch.randint(0, 256, (E, N, K // 2), dtype=torch.uint8, device="cuda", generator=gen)
-    s = torch.randint(0, 256, (E, N, K // 16), dtype=torch.uint8, device="cuda", generator=gen)
-    s = torch.where((s & 0x7F) == 0x7F, s - 1, s)
+    s = torch.randint(0, 127, (E, N, K // 16), dtype=torch.uint8, device="cuda", generator=gen)
     s2 = torch.rand(E, device="cuda", generator=gen) * 1e-3
     return w, s, s2
 
@@ -54,7 +54,8 @@ def expected(x, idx, w, s, s2, relu2, dtype):
                 continue
             W, v = dense(w, s, s2, e), (x[t, j] if x.dim() == 3 else x[t]).double()
             ref[t, j] = W @ v
-            d[t, j] = K * 2.0 ** -23 * (W.abs() @ v.abs()) + W.abs().sum(1) * v.abs().max() * 2.0 ** -39
+            d[t, j] = (K + 8) * 2.0 ** -23 * 3 * (W.abs() @ v.abs()) + (
+                W.abs().sum(1) * v.abs().max() * 2.0 ** -22)
     d = d + ref.abs() * 2.0 ** -24
     if relu2:
         d = 2 * ref.clamp(min=0) * d + d * d
@@ -133,7 +134,8 @@ def test_ids_out_of_range_give_zero_rows():
 
 
 def test_every_code_and_scale():
-    # a single 1 in the token reads one weight: 16 codes x every finite scale, exactly
+    # a single 1 in the token reads one weight: 16 codes x every finite scale, exactly; the sign
+    # bit of a scale is ignored
     codes = torch.arange(16, dtype=torch.uint8, device="cuda")
     scales = torch.tensor([b for b in range(256) if b & 0x7F != 0x7F], dtype=torch.uint8, device="cuda")
     N, K = scales.numel(), 64
@@ -147,7 +149,7 @@ def test_every_code_and_scale():
     y = torch.zeros(1, 16, N, dtype=torch.float16, device="cuda")
     moe.nvfp4_gemv(x, idx, w, s, s2, y)
     table = torch.tensor(E2M1 + tuple(-v for v in E2M1), dtype=torch.float64, device="cuda")
-    ref = table.view(16, 1) * scales.view(torch.float8_e4m3fn).double().view(1, N)
+    ref = table.view(16, 1) * scales.view(torch.float8_e4m3fn).double().abs().view(1, N)
     assert torch.equal(y[0].double(), ref + 0.0)
 
 
