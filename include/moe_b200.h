@@ -354,7 +354,7 @@ MOE_API moe_status moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const vo
  * Weights and scales are exact, an element of x counts to 2^-22 of its row's
  * largest, sums are float32 and the result is rounded once.  Infinities and
  * NaN behave as in the formula (a row that holds one takes a slow path).
- * The weights are read once per 8 rows of an expert (4 in small batches).
+ * The weights are read once per 4 rows of an expert.
  *
  * The call keeps no state and uses no workspace: it allocates nothing, may be
  * captured in a CUDA graph and may overlap in time with others.  y must not

@@ -21,17 +21,20 @@
 // Infinities and NaN have no digits: they count as zero there and are added
 // in the epilogue from the stored weights.
 //
-// Layout: routed rows of one expert share passes of up to `rp` rows over its
+// Layout: routed rows of one expert share passes of up to 4 rows over its
 // matrix.  All passes' blocks of 64 weight rows ("units") form one list, cut
 // into contiguous ranges, one per CTA; a CTA takes two neighbouring units of a
 // pass as one tile of 128 rows (the MMA's M) where it can.
-//   warp 0     TMA: 256 inputs (128 bytes) of a tile's rows into a ring stage;
-//   warp 1     scales from shared memory into TMEM (tcgen05.cp) and the MMAs;
+//   warp 12    TMA: 256 inputs (128 bytes) of a tile's rows into a ring stage;
+//   warps 0-3  the MMAs, every fourth stage of a tile each and into an
+//              accumulator of its own: a thread takes 1300 cycles to wait for a
+//              stage and issue its four MMAs, the MMAs themselves about 600;
 //   warps 4-7  epilogue: a lane is a weight row, so the lanes' results are
 //              neighbours in y;
-//   warps 8-11 scales from global memory into the ring, in the order of
-//              tcgen05.cp (rows are K / 16 bytes apart, which no tensor map
-//              takes);
+//   warps 8-11 scales from global memory through registers into TMEM, a lane
+//              quarter each (rows are K / 16 bytes apart, which no tensor map
+//              takes; through shared memory and tcgen05.cp a stage's four
+//              copies and their hand-over took longer than its MMAs);
 //   warps 4-11 the token rows' digits, at the start of each pass.
 // Results do not depend on the grid.
 #include <cuda_fp16.h>
@@ -42,22 +45,24 @@
 namespace moe {
 namespace {
 
-constexpr int kGemvThreads = 384;
+constexpr int kGemvThreads = 416;
 constexpr int kUnitRows = 64;
 constexpr int kDigits = 8;
-constexpr int kMaxPassRows = 8;
+constexpr int kMaxPassRows = 4;
 constexpr int kStageK = 256;         // inputs of a stage: 128 bytes a row
-constexpr int kStageA = 128 * 128;   // a stage's weights
-constexpr int kStageSf = 4 * 512;    // and their scales: a 512-byte block per 64 inputs
-constexpr int kStageBytes = kStageA + kStageSf;
-constexpr int kMaxStages = 11;
+constexpr int kStageBytes = 128 * 128;  // a stage's weights
+constexpr int kMaxStages = 12;
 constexpr int kMaxRows = MOE_NVFP4_MAX_ROWS;
 constexpr int kGemvSmemMax = 232448;
-// TMEM columns: two accumulators, the tokens' scales (ones), the stages' scales
-constexpr uint32_t kColSfb = 2 * kMaxPassRows * kDigits;
-constexpr uint32_t kColSfa = kColSfb + 4;
+// TMEM columns: two accumulators (of kChains each), the tokens' scales (ones),
+// the stages' scales (16 columns each: 4 bytes of a row per 64 inputs, 4 x 32 rows)
+constexpr int kChains = 4;  // MMA warps
+constexpr uint32_t kAccCols = kMaxPassRows * kDigits;
+constexpr uint32_t kColSfb = 2 * kChains * kAccCols;
+constexpr uint32_t kColSfa = kColSfb + 16;
 constexpr uint32_t kTmemCols = 512;
 static_assert(kColSfa + kMaxStages * 16 <= kTmemCols, "");
+constexpr int kAhead = 3;            // stages whose scales are under way in registers
 constexpr int kConverters = 8 * 32;  // threads that write digits (warps 4-11)
 
 struct GemvArgs {
@@ -75,7 +80,7 @@ struct GemvArgs {
   void* y;
   long long ldy;
   int* status;
-  int rp;      // rows of a pass, at most (1, 2, 4 or 8)
+  int rp;      // rows of a pass, at most (1, 2 or 4)
   int xrows;   // digit rows kept in shared memory: max(rp * 8, 16)
   int stages;
 };
@@ -126,17 +131,6 @@ __device__ __forceinline__ void umma_nvfp4(uint32_t d, uint64_t adesc, uint64_t 
 // scales (bit 23 clear), scale ids 0, M = 128.
 __device__ __forceinline__ uint32_t nvfp4_idesc(uint32_t N) {
   return (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((128u >> 4) << 24);
-}
-
-// 32 rows of 16 bytes (512 contiguous bytes of shared memory) to 4 TMEM
-// columns of lanes 0-31, and the same to the other three lane quarters.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t smem) {
-  uint64_t d = 0;
-  d |= uint64_t((smem >> 4) & 0x3FFFu);
-  d |= uint64_t(128 >> 4) << 16;
-  d |= uint64_t(128 >> 4) << 32;  // eight rows are 128 bytes
-  d |= uint64_t(1) << 46;         // version; no swizzle
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 
 __device__ __forceinline__ int expert_of(const GemvArgs& p, int r) {
@@ -232,8 +226,7 @@ __device__ __forceinline__ void group_rows(const GemvArgs& p, Setup& S) {
 
 // Eight elements of a token row in float32.
 template <bool BF16>
-__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void to_float8(const uint4& u, float (&v)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -249,6 +242,19 @@ __device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
 }
 
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.4028235e38f; }
+
+// Their largest finite magnitude into m; bad: one is not finite.
+template <bool BF16>
+__device__ __forceinline__ void amax8(const uint4& u, float& m, int& bad) {
+  float v[8];
+  to_float8<BF16>(u, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool f = finite(v[i]);
+    m = fmaxf(m, f ? fabsf(v[i]) : 0.f);
+    bad |= !f;
+  }
+}
 
 __device__ __forceinline__ float pow2(int e) {  // e in -126..127
   return __uint_as_float(uint32_t(e + 127) << 23);
@@ -293,35 +299,37 @@ __device__ __forceinline__ void transpose_nibbles(uint32_t (&w)[8]) {
   }
 }
 
-// 16 scale bytes of one weight row from byte `at` on, zeros from `n` valid
-// ones on; `align` is the largest power of two (2..16) that divides every
-// row's address.
-__device__ __forceinline__ uint4 load_scales(const uint8_t* p, int n, int align) {
-  uint4 u = make_uint4(0, 0, 0, 0);
-  if (n >= 16 && align == 16) return *reinterpret_cast<const uint4*>(p);
-  if (align >= 8) {
-    if (n >= 8) {
-      const uint2 a = *reinterpret_cast<const uint2*>(p);
-      u.x = a.x, u.y = a.y;
-    }
-    if (n >= 16) {
-      const uint2 a = *reinterpret_cast<const uint2*>(p + 8);
-      u.z = a.x, u.w = a.y;
-    }
-    if ((n & 7) == 0) return u;
-  } else if (align == 4) {
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
-    if (n >= 4) u.x = q[0];
-    if (n >= 8) u.y = q[1];
-    if (n >= 12) u.z = q[2];
-    if (n >= 16) u.w = q[3];
-    if ((n & 3) == 0) return u;
-  }
-  const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
-  uint32_t h[8];
+// Sixteen scale bytes of a weight row, in pieces of W bytes (the alignment
+// every row keeps).  Pieces that do not exist are read from the row's last
+// one and cleared when the scales are used: straight-line loads, so that a
+// thread has those of several stages under way (with the bounds decided at
+// the load, each waited for its data: 1000 cycles a stage).
+template <int W>
+__device__ __forceinline__ void load_scales(const uint8_t* row, int at, int row_bytes,
+                                            uint32_t (&v)[4]) {
+  if constexpr (W == 16) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + at));
+    v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+  } else if constexpr (W == 8) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = 2 * i < n ? q[i] : 0;
-  return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    for (int i = 0; i < 2; ++i) {
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + min(at + 8 * i, row_bytes - 8)));
+      v[2 * i] = u.x, v[2 * i + 1] = u.y;
+    }
+  } else if constexpr (W == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = __ldg(reinterpret_cast<const uint32_t*>(row + min(at + 4 * i, row_bytes - 4)));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo =
+          __ldg(reinterpret_cast<const uint16_t*>(row + min(at + 4 * i, row_bytes - 2)));
+      const uint32_t hi =
+          __ldg(reinterpret_cast<const uint16_t*>(row + min(at + 4 * i + 2, row_bytes - 2)));
+      v[i] = lo | hi << 16;
+    }
+  }
 }
 
 // What the infinities and NaN of a token row add to weight row `row`.
@@ -343,21 +351,19 @@ __device__ __noinline__ float odd_part(const GemvArgs& p, const uint16_t* x, lon
   return sum;
 }
 
-template <bool BF16>
+template <bool BF16, int W>
 __global__ void __launch_bounds__(kGemvThreads, 1)
     nvfp4_gemv_kernel(const __grid_constant__ GemvArgs p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Setup S;
   __shared__ uint64_t full[kMaxStages], sf_full[kMaxStages], empty[kMaxStages];
-  __shared__ uint64_t tfull[2], tempty[2], xfull, drain;
+  __shared__ uint64_t tfull[2], tempty[2], xfull, drain[kChains];
   __shared__ uint32_t tmem_slot;
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
-  uint8_t* ring = smem_raw + pad;                 // stages: weights, then all stages' scales
-  uint8_t* sf = ring + p.stages * kStageA;
-  uint8_t* xs = sf + p.stages * kStageSf;         // the digits
+  uint8_t* ring = smem_raw + pad;                 // the stages
+  uint8_t* xs = ring + p.stages * kStageBytes;    // the digits
   const int nst = (p.K + kStageK - 1) / kStageK;  // stages of a tile
   const int xblock = p.xrows * 128;               // digit rows of one stage's inputs
-  uint8_t* ones = xs + nst * xblock;              // 512 bytes: the tokens' scales
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -367,22 +373,20 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&tfull[b], 1);
+      mbar_init(&tfull[b], kChains);
       mbar_init(&tempty[b], 4);
     }
     mbar_init(&xfull, 1);
-    mbar_init(&drain, 1);
+    for (int c = 0; c < kChains; ++c) mbar_init(&drain[c], 1);
     fence_barrier_init();
     tma_prefetch_desc(&p.tmW);
     S.abort = 0;
   }
-  if (warp == 1) {
+  if (warp == 12) {
     tmem_alloc(&tmem_slot, kTmemCols);
     tmem_relinquish();
   }
-  if (tid >= 128 && tid < 256) reinterpret_cast<uint32_t*>(ones)[tid - 128] = 0x38383838u;
   if (tid < kMaxPassRows) S.xrow[tid] = -2;
-  fence_proxy_async_smem();
   pdl_wait();
   pdl_trigger();
   // ---- passes: routed rows grouped by expert, at most rp rows each
@@ -412,7 +416,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
 
   // Every role walks the same tiles: u -> pass, first unit inside the pass,
   // two units where this CTA has both of a pass.
-  if (warp == 0) {
+  if (warp == 12) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       int stage = 0;
@@ -429,7 +433,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
           }
           mbar_arrive_expect_tx(&full[stage], two * 8192);
           for (int h = 0; h < two; ++h)
-            tma_load_3d<1>(smem_u32(ring + stage * kStageA + h * 8192), &p.tmW,
+            tma_load_3d<1>(smem_u32(ring + stage * kStageBytes + h * 8192), &p.tmW,
                            smem_u32(&full[stage]), k * 128, row + h * kUnitRows, 0);
           if (++stage == p.stages) {
             stage = 0;
@@ -443,12 +447,11 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
         }
       }
     }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------- MMA issuer
+  } else if (warp < kChains) {
+    // --------------------------------------------------------- MMA issuers
     if (lane == 0) {
-      tmem_cp_scales(tmem + kColSfb, smem_u32(ones));
-      int stage = 0, it = 0, seen = -1;
-      uint32_t phase = 0, xphase = 0;
+      int base = 0, it = 0, seen = -1;  // stages before the tile, tiles, pass
+      uint32_t xphase = 0;
       bool ok = true;
       for (int u = u0, two; u < u1 && ok; u += two) {
         const int pass = u / blocks, block = u - pass * blocks;
@@ -460,10 +463,12 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
         }
         const int cols = max(16, (S.pass_n[pass] * kDigits + 15) & ~15);
         const uint32_t idesc = nvfp4_idesc(cols);
-        const uint32_t d = tmem + uint32_t((it & 1) * kMaxPassRows * kDigits);
+        const uint32_t d = tmem + uint32_t((it & 1) * kChains + warp) * kAccCols;
         if (!wait_for(p, &tempty[it & 1], ((it >> 1) & 1) ^ 1u, &S.abort)) break;
         tc_fence_after();
-        for (int k = 0; k < nst; ++k) {
+        for (int k = warp; k < nst; k += kChains) {
+          const int stage = (base + k) % p.stages;
+          const uint32_t phase = ((base + k) / p.stages) & 1;
           if (!wait_for(p, &full[stage], phase, &S.abort) ||
               !wait_for(p, &sf_full[stage], phase, &S.abort)) {
             ok = false;
@@ -472,38 +477,52 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
           tc_fence_after();
           const uint32_t sfa = tmem + kColSfa + stage * 16;
           const int steps = min(4, (p.K - k * kStageK + 63) / 64);
-          for (int j = 0; j < steps; ++j)
-            tmem_cp_scales(sfa + j * 4, smem_u32(sf + stage * kStageSf + j * 512));
-          const uint64_t ad = smem_desc_sw128(ring + stage * kStageA);
+          const uint64_t ad = smem_desc_sw128(ring + stage * kStageBytes);
           const uint64_t bd = smem_desc_sw128(xs + k * xblock);
-          for (int j = 0; j < steps; ++j)
-            umma_nvfp4(d, ad + j * 2, bd + j * 2, idesc, sfa + j * 4, tmem + kColSfb,
-                       (k | j) ? 1u : 0u);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < steps)
+              umma_nvfp4(d, ad + j * 2, bd + j * 2, idesc, sfa + j * 4, tmem + kColSfb,
+                         k >= kChains || j > 0);
           umma_commit(&empty[stage]);
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
         if (ok) umma_commit(&tfull[it & 1]);
+        base += nst;
         ++it;
       }
-      umma_commit(&drain);
+      umma_commit(&drain[warp]);
       int zero = 0;
-      mbar_wait(&drain, 0, &zero);
+      mbar_wait(&drain[warp], 0, &zero);
     }
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------- digits, then epilogue or scales
     const int cw = warp - 4;
     int stage = 0, it = 0;
     uint32_t phase = 0;
     const int row_bytes = p.K / 16;
-    const int align = min(16, row_bytes & -row_bytes);
     for (int ub = u0; ub < u1;) {
       const int pass = ub / blocks;
       const int ue = min(u1, (pass + 1) * blocks);  // this CTA's units of the pass
       const int n_rows = S.pass_n[pass], e = S.pass_e[pass];
       const int16_t* rows = S.sorted + S.pass_at[pass];
+      // warps 8-11: the first scales are under way while the digits are made
+      int lu = ub, lk = 0;  // unit and stage of the next load
+      auto load = [&](uint32_t (&v)[4][4]) {
+        const int first = (min(lu, ue - 1) - pass * blocks) * kUnitRows + lane;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          load_scales<W>(p.scale + ((long long)(e)*p.N + min(first + 32 * c, p.N - 1)) * row_bytes,
+                         lk * 16, row_bytes, v[c]);
+        if (++lk == nst) {
+          lk = 0;
+          lu += 2;
+        }
+      };
+      uint32_t next[kAhead][4][4];
+      if (warp >= 8) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) load(next[i]);
+      }
       {
         // a row's 256-wide blocks over 8, 4, 2 or 1 warps
         const int per = n_rows > 4 ? 1 : n_rows > 2 ? 2 : n_rows > 1 ? 4 : 8;
@@ -515,21 +534,21 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
         named_barrier(1, kConverters);
         if (S.changed == pass) {
           const uint16_t* xr = static_cast<const uint16_t*>(p.x) + (want < 0 ? 0 : want) * p.ldx;
+          // a lane's first two chunks of 8 elements stay in registers
+          const int k0 = part * 256 + lane * 8, kstep = per * 256;
+          uint4 held[2];
           if (want >= 0) {
             float m = 0.f;
             int bad = 0;
-#pragma unroll 2
-            for (int k = part * 256 + lane * 8; k < p.K; k += per * 256) {
-              float v[8];
-              load8<BF16>(xr + k, v);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                if (finite(v[i]))
-                  m = fmaxf(m, fabsf(v[i]));
-                else
-                  bad = 1;
-              }
-            }
+            for (int i = 0; i < 2; ++i)
+              held[i] = k0 + i * kstep < p.K
+                            ? *reinterpret_cast<const uint4*>(xr + k0 + i * kstep)
+                            : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) amax8<BF16>(held[i], m, bad);
+            for (int k = k0 + 2 * kstep; k < p.K; k += kstep)
+              amax8<BF16>(*reinterpret_cast<const uint4*>(xr + k), m, bad);
 #pragma unroll
             for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
             bad = __any_sync(0xffffffffu, bad);
@@ -556,21 +575,28 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
               S.shift[n] = sh;
               S.odd[n] = bad;
             }
-            for (int k = part * 256 + lane * 8; k < nst * kStageK; k += per * 256) {
-              uint32_t w[8] = {};
-              if (k < p.K) {
-                float v[8];
-                load8<BF16>(xr + k, v);
+            auto put = [&](int k, const uint4& u) {
+              uint32_t w[8];
+              float v[8];
+              to_float8<BF16>(u, v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  w[i] = digit_codes(finite(v[i]) ? __float2int_rn(v[i] * f1 * f2) : 0);
-                transpose_nibbles(w);
-              }
+              for (int i = 0; i < 8; ++i)
+                w[i] = digit_codes(finite(v[i]) ? __float2int_rn(v[i] * f1 * f2) : 0);
+              transpose_nibbles(w);
               // digit i of eight inputs: 4 bytes of row n * 8 + i, swizzled as TMA would
               uint8_t* dst = xs + (k / kStageK) * xblock + n * kDigits * 128 + (lane & 3) * 4;
 #pragma unroll
               for (int i = 0; i < kDigits; ++i)
                 *reinterpret_cast<uint32_t*>(dst + i * 128 + ((lane >> 2) ^ i) * 16) = w[i];
+            };
+            // zeros behind K, to the end of the last stage
+            // (one copy of the code: it runs cold)
+#pragma unroll 1
+            for (int k = k0, i = 0; k < nst * kStageK; k += kstep, ++i) {
+              uint4 u = i == 0 ? held[0] : held[1];
+              if (i > 1)
+                u = k < p.K ? *reinterpret_cast<const uint4*>(xr + k) : make_uint4(0, 0, 0, 0);
+              put(k, u);
             }
           }
           fence_proxy_async_smem();
@@ -578,25 +604,34 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
         }
         if (warp == 4 && lane == 0) mbar_arrive(&xfull);
       }
-      const float s2 = p.scale2[e];
-      for (int u = ub, two; u < ue; u += two) {
-        two = u + 1 < ue ? 2 : 1;
-        const int n0 = (u - pass * blocks) * kUnitRows;
-        const int valid = min(two * kUnitRows, p.N - n0);  // weight rows of the tile
-        if (warp < 8) {
-          // -------------------------------------------------------- epilogue
+      if (warp < 8) {
+        // ---------------------------------------------------------- epilogue
+        const float s2 = p.scale2[e];
+        const int chains = min(kChains, nst);  // accumulators in use
+        for (int u = ub, two; u < ue; u += two) {
+          two = u + 1 < ue ? 2 : 1;
+          const int n0 = (u - pass * blocks) * kUnitRows;
+          const int valid = min(two * kUnitRows, p.N - n0);  // weight rows of the tile
           const int r = cw * 32 + lane;
           const bool ok = wait_for(p, &tfull[it & 1], (it >> 1) & 1, &S.abort);
           tc_fence_after();
           const uint32_t d = tmem + (uint32_t(cw * 32) << 16) +
-                             uint32_t((it & 1) * kMaxPassRows * kDigits);
+                             uint32_t(it & 1) * kChains * kAccCols;
           for (int n = 0; n < n_rows && cw * 32 < valid; ++n) {
-            uint32_t acc[1][kDigits];
-            tmem_ld_32x32b_n<kDigits>(d + uint32_t(n * kDigits), acc[0]);
-            tmem_ld_wait_regs(acc);
-            float v = __uint_as_float(acc[0][kDigits - 1]);
+            uint32_t acc[kChains][kDigits];
 #pragma unroll
-            for (int i = kDigits - 2; i >= 0; --i) v = fmaf(v, 8.f, __uint_as_float(acc[0][i]));
+            for (int c = 0; c < kChains; ++c)
+              tmem_ld_32x32b_n<kDigits>(d + c * kAccCols + uint32_t(n * kDigits), acc[c]);
+            tmem_ld_wait_regs(acc);
+            float v = 0.f;
+#pragma unroll
+            for (int i = kDigits - 1; i >= 0; --i) {
+              float t = __uint_as_float(acc[0][i]);
+#pragma unroll
+              for (int c = 1; c < kChains; ++c)
+                if (c < chains) t += __uint_as_float(acc[c][i]);
+              v = fmaf(v, 8.f, t);
+            }
             // digits count halves: times 2^(1 - s), in whatever range the factors lie
             const double unscale =
                 __longlong_as_double((long long)(1023 + 1 - S.shift[n]) << 52);
@@ -619,27 +654,47 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&tempty[it & 1]);
           ++it;
-        } else {
-          // ---------------------------------------------------------- scales
-          const int r = (cw - 4) * 32 + lane;  // weight row of the tile
-          const uint8_t* src = p.scale + ((long long)(e)*p.N + n0 + r) * row_bytes;
-          auto load = [&](int k) {
-            return r < valid ? load_scales(src + k * 16, min(16, row_bytes - k * 16), align)
-                             : make_uint4(0, 0, 0, 0);
-          };
-          uint4 next = load(0);
-          for (int k = 0; k < nst; ++k) {
-            const uint4 v = next;
-            if (k + 1 < nst) next = load(k + 1);
+        }
+      } else {
+        // ------------------------------------------------------------ scales
+        // Each warp fills its own lane quarter of TMEM, and every quarter holds
+        // all rows' scales: lane l keeps those of rows l, l + 32, l + 64 and
+        // l + 96, for the next kAhead stages, in registers.
+        const uint32_t quarter = tmem + (uint32_t((cw & 3) * 32) << 16);
+        if (ub == u0) {
+          uint32_t ones[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) ones[i] = 0x38383838u;
+          tmem_st_32x32b_x16(quarter + kColSfb, ones);
+        }
+        const int total = (ue - ub + 1) / 2 * nst;
+        int su = ub, sk = 0;  // unit and stage of the next store
+        for (int q = 0; q < total; q += kAhead) {
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            if (q + i >= total) break;
+            // scales are unsigned; none behind K or the tile's last row
+            const int valid = min((su + 1 < ue ? 2 : 1) * kUnitRows,
+                                  p.N - (su - pass * blocks) * kUnitRows);
+            uint32_t v[16];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int left = row_bytes - sk * 16 - 4 * j;  // 2 where K ends inside
+              const uint32_t keep = left >= 4 ? 0x7F7F7F7Fu : left > 0 ? 0x7F7Fu : 0u;
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                v[4 * j + c] = lane + 32 * c < valid ? next[i][c][j] & keep : 0u;
+            }
+            load(next[i]);
+            if (++sk == nst) {
+              sk = 0;
+              su += 2;
+            }
             wait_for(p, &empty[stage], phase ^ 1u, &S.abort);
-            // row r of a 64-input block: bytes (r % 32) * 16 + (r / 32) * 4
-            uint32_t* dst =
-                reinterpret_cast<uint32_t*>(sf + stage * kStageSf) + lane * 4 + (cw - 4);
-            dst[0] = v.x & 0x7F7F7F7Fu;  // scales are unsigned
-            dst[128] = v.y & 0x7F7F7F7Fu;
-            dst[256] = v.z & 0x7F7F7F7Fu;
-            dst[384] = v.w & 0x7F7F7F7Fu;
-            fence_proxy_async_smem();
+            tc_fence_after();
+            tmem_st_32x32b_x16(quarter + kColSfa + stage * 16, v);
+            tmem_st_wait();
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sf_full[stage]);
             if (++stage == p.stages) {
@@ -654,7 +709,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 12) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -663,12 +718,12 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
 // Static shared memory of the kernel, at most.
 constexpr int kGemvStatic = int(sizeof(Setup)) + 512;
 
-template <bool BF16>
+template <bool BF16, int W>
 cudaError_t launch_gemv(const GemvArgs& a, int dev, int grid, int smem, cudaStream_t stream) {
   static std::atomic<bool> ready[kMaxDevices];
   if (!ready[dev].load(std::memory_order_acquire)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(nvfp4_gemv_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(nvfp4_gemv_kernel<BF16, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kGemvSmemMax - kGemvStatic);
     if (e != cudaSuccess) return e;
     ready[dev].store(true, std::memory_order_release);
@@ -685,7 +740,14 @@ cudaError_t launch_gemv(const GemvArgs& a, int dev, int grid, int smem, cudaStre
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, nvfp4_gemv_kernel<BF16>, a);
+  return cudaLaunchKernelEx(&cfg, nvfp4_gemv_kernel<BF16, W>, a);
+}
+
+template <int W>
+cudaError_t launch_any(bool bf16, const GemvArgs& a, int dev, int grid, int smem,
+                       cudaStream_t stream) {
+  return bf16 ? launch_gemv<true, W>(a, dev, grid, smem, stream)
+              : launch_gemv<false, W>(a, dev, grid, smem, stream);
 }
 
 }  // namespace
@@ -741,14 +803,12 @@ extern "C" moe_status moe_nvfp4_gemv(const void* x, int64_t ldx, int32_t x_per_s
   a.y = y;
   a.ldy = ldy;
   a.status = status;
-  // Rows of a pass: as many as an expert can have when ids are distinct, but
-  // at most 4 while the experts see fewer than 4 rows on average (their
-  // digits take shared memory from the ring), else 8, and fewer where the
-  // digits would leave less than four stages.
-  a.rp = num_tokens > 4 ? 8 : num_tokens > 2 ? 4 : num_tokens;
-  if (a.rp == 8 && a.R < 4 * num_experts) a.rp = 4;
+  // Rows of a pass: as many as an expert can have when ids are distinct, at
+  // most 4 (their digits take shared memory from the ring and accumulator
+  // columns), fewer where the digits would leave less than four stages.
+  a.rp = num_tokens > 2 ? kMaxPassRows : num_tokens;
   const int nst = (K + kStageK - 1) / kStageK;
-  const int room = kGemvSmemMax - kGemvStatic - 1024 - 512;
+  const int room = kGemvSmemMax - kGemvStatic - 1024;
   for (;; a.rp /= 2) {
     a.xrows = a.rp * kDigits < 16 ? 16 : a.rp * kDigits;
     a.stages = (room - nst * a.xrows * 128) / kStageBytes;
@@ -757,10 +817,14 @@ extern "C" moe_status moe_nvfp4_gemv(const void* x, int64_t ldx, int32_t x_per_s
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   const long long most = (long long)(a.R) * ((N + kUnitRows - 1) / kUnitRows);
   const int grid = int(most < sms ? most : sms);
-  const int smem = 1024 + a.stages * kStageBytes + nst * a.xrows * 128 + 512;
+  const int smem = 1024 + a.stages * kStageBytes + nst * a.xrows * 128;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t err = dtype == MOE_DTYPE_BF16 ? launch_gemv<true>(a, dev, grid, smem, cs)
-                                                  : launch_gemv<false>(a, dev, grid, smem, cs);
+  const bool bf16 = dtype == MOE_DTYPE_BF16;
+  const int row_bytes = K / 16;  // of scales: even
+  const cudaError_t err = row_bytes % 16 == 0  ? launch_any<16>(bf16, a, dev, grid, smem, cs)
+                          : row_bytes % 8 == 0 ? launch_any<8>(bf16, a, dev, grid, smem, cs)
+                          : row_bytes % 4 == 0 ? launch_any<4>(bf16, a, dev, grid, smem, cs)
+                                               : launch_any<2>(bf16, a, dev, grid, smem, cs);
   if (err != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;

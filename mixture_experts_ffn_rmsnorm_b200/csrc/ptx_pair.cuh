@@ -183,6 +183,20 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t m0, ui
                : "memory");
 }
 
+// 32 lanes x 16 consecutive 32-bit TMEM columns from registers (this warp's
+// lane quarter), and the wait for this thread's TMEM stores.
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 // Makes this thread's shared-memory stores visible to the async proxy
 // (tcgen05.mma operands, TMA).
 __device__ __forceinline__ void fence_proxy_async_smem() {
