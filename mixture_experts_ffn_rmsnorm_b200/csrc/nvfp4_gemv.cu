@@ -25,16 +25,17 @@
 // matrix.  All passes' blocks of 64 weight rows ("units") form one list, cut
 // into contiguous ranges, one per CTA; a CTA takes two neighbouring units of a
 // pass as one tile of 128 rows (the MMA's M) where it can.
-//   warp 12    TMA: 256 inputs (128 bytes) of a tile's rows into a ring stage;
+//   warp 16    TMA: 256 inputs (128 bytes) of a tile's rows into a ring stage,
+//              and the tile's scales as one copy;
 //   warps 0-3  the MMAs, every fourth stage of a tile each and into an
 //              accumulator of its own: a thread takes 1300 cycles to wait for a
 //              stage and issue its four MMAs, the MMAs themselves about 600;
 //   warps 4-7  epilogue: a lane is a weight row, so the lanes' results are
 //              neighbours in y;
-//   warps 8-11 scales from global memory through registers into TMEM, a lane
-//              quarter each (rows are K / 16 bytes apart, which no tensor map
-//              takes; through shared memory and tcgen05.cp a stage's four
-//              copies and their hand-over took longer than its MMAs);
+//   warps 12-15 scales from shared memory through registers into TMEM, a
+//              lane quarter each (read from global memory by the row, 4 to 8
+//              bytes a lane, they took 1000 cycles a stage; handed on with
+//              tcgen05.cp, the four copies of a stage held up its MMAs);
 //   warps 4-11 the token rows' digits, at the start of each pass.
 // Results do not depend on the grid.
 #include <cuda_fp16.h>
@@ -45,7 +46,8 @@
 namespace moe {
 namespace {
 
-constexpr int kGemvThreads = 416;
+constexpr int kGemvThreads = 544;
+constexpr int kProducer = 16;  // warp
 constexpr int kUnitRows = 64;
 constexpr int kDigits = 8;
 constexpr int kMaxPassRows = 4;
@@ -62,7 +64,6 @@ constexpr uint32_t kColSfb = 2 * kChains * kAccCols;
 constexpr uint32_t kColSfa = kColSfb + 16;
 constexpr uint32_t kTmemCols = 512;
 static_assert(kColSfa + kMaxStages * 16 <= kTmemCols, "");
-constexpr int kAhead = 3;            // stages whose scales are under way in registers
 constexpr int kConverters = 8 * 32;  // threads that write digits (warps 4-11)
 
 struct GemvArgs {
@@ -73,6 +74,7 @@ struct GemvArgs {
   const int* idx;
   int R, top_k;
   const uint8_t* scale;
+  long long scale_bytes;  // E * N * K / 16
   const float* scale2;
   const uint8_t* w;
   int E, K, N;
@@ -83,6 +85,8 @@ struct GemvArgs {
   int rp;      // rows of a pass, at most (1, 2 or 4)
   int xrows;   // digit rows kept in shared memory: max(rp * 8, 16)
   int stages;
+  int raws;       // tiles whose scales are in shared memory (1 or 2)
+  int raw_bytes;  // of one tile
 };
 
 static_assert(kMaxRows <= 32767 && MOE_MAX_EXPERTS <= 256, "int16 / uint8 tables");
@@ -299,37 +303,43 @@ __device__ __forceinline__ void transpose_nibbles(uint32_t (&w)[8]) {
   }
 }
 
-// Sixteen scale bytes of a weight row, in pieces of W bytes (the alignment
-// every row keeps).  Pieces that do not exist are read from the row's last
-// one and cleared when the scales are used: straight-line loads, so that a
-// thread has those of several stages under way (with the bounds decided at
-// the load, each waited for its data: 1000 cycles a stage).
+// Sixteen scale bytes of a weight row in shared memory, in pieces of W bytes
+// (the alignment every row keeps).  Pieces behind the row's end are read from
+// its last one; the caller clears them.
 template <int W>
 __device__ __forceinline__ void load_scales(const uint8_t* row, int at, int row_bytes,
                                             uint32_t (&v)[4]) {
   if constexpr (W == 16) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + at));
+    const uint4 u = *reinterpret_cast<const uint4*>(row + at);
     v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
   } else if constexpr (W == 8) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + min(at + 8 * i, row_bytes - 8)));
+      const uint2 u = *reinterpret_cast<const uint2*>(row + min(at + 8 * i, row_bytes - 8));
       v[2 * i] = u.x, v[2 * i + 1] = u.y;
     }
   } else if constexpr (W == 4) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      v[i] = __ldg(reinterpret_cast<const uint32_t*>(row + min(at + 4 * i, row_bytes - 4)));
+      v[i] = *reinterpret_cast<const uint32_t*>(row + min(at + 4 * i, row_bytes - 4));
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t lo =
-          __ldg(reinterpret_cast<const uint16_t*>(row + min(at + 4 * i, row_bytes - 2)));
+      const uint32_t lo = *reinterpret_cast<const uint16_t*>(row + min(at + 4 * i, row_bytes - 2));
       const uint32_t hi =
-          __ldg(reinterpret_cast<const uint16_t*>(row + min(at + 4 * i + 2, row_bytes - 2)));
+          *reinterpret_cast<const uint16_t*>(row + min(at + 4 * i + 2, row_bytes - 2));
       v[i] = lo | hi << 16;
     }
   }
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
 }
 
 // What the infinities and NaN of a token row add to weight row `row`.
@@ -357,13 +367,15 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ Setup S;
   __shared__ uint64_t full[kMaxStages], sf_full[kMaxStages], empty[kMaxStages];
-  __shared__ uint64_t tfull[2], tempty[2], xfull, drain[kChains];
+  __shared__ uint64_t tfull[2], tempty[2], raw_full[2], raw_empty[2], xfull, drain[kChains];
   __shared__ uint32_t tmem_slot;
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* ring = smem_raw + pad;                 // the stages
   uint8_t* xs = ring + p.stages * kStageBytes;    // the digits
   const int nst = (p.K + kStageK - 1) / kStageK;  // stages of a tile
   const int xblock = p.xrows * 128;               // digit rows of one stage's inputs
+  uint8_t* raw = xs + nst * xblock;               // tiles' scales as they are stored
+  const int row_bytes = p.K / 16;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -375,6 +387,8 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], kChains);
       mbar_init(&tempty[b], 4);
+      mbar_init(&raw_full[b], 1);
+      mbar_init(&raw_empty[b], 4);
     }
     mbar_init(&xfull, 1);
     for (int c = 0; c < kChains; ++c) mbar_init(&drain[c], 1);
@@ -382,7 +396,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     tma_prefetch_desc(&p.tmW);
     S.abort = 0;
   }
-  if (warp == 12) {
+  if (warp == kProducer) {
     tmem_alloc(&tmem_slot, kTmemCols);
     tmem_relinquish();
   }
@@ -410,22 +424,42 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
   }
 
   const int blocks = (p.N + kUnitRows - 1) / kUnitRows;
-  const long long units = (long long)(S.passes) * blocks;
+  // (at most 1024 * 2048 units: 32 bits hold their product with the grid)
+  const uint32_t units = uint32_t(S.passes) * uint32_t(blocks);
   const int u0 = int(units * blockIdx.x / gridDim.x);
   const int u1 = int(units * (blockIdx.x + 1) / gridDim.x);
 
   // Every role walks the same tiles: u -> pass, first unit inside the pass,
   // two units where this CTA has both of a pass.
-  if (warp == 12) {
+  if (warp == kProducer) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int stage = 0;
+      int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int u = u0, two; u < u1 && ok; u += two) {
         const int pass = u / blocks, block = u - pass * blocks;
         two = u + 1 < u1 && block + 1 < blocks ? 2 : 1;
         const int row = S.pass_e[pass] * p.N + block * kUnitRows;
+        {
+          // the rows' scales: the 16-byte blocks that hold them, and the
+          // tensor's last bytes, fewer than 16, by plain loads
+          const int slot = it % p.raws;
+          if (!wait_for(p, &raw_empty[slot], ((it / p.raws) & 1) ^ 1u, &S.abort)) {
+            ok = false;
+            break;
+          }
+          const long long a = (long long)(row)*row_bytes;
+          const long long end = a + min(two * kUnitRows, p.N - block * kUnitRows) * row_bytes;
+          const long long a16 = a & ~15LL, whole = p.scale_bytes & ~15LL;
+          const long long b16 = min((end + 15) & ~15LL, whole);
+          uint8_t* dst = raw + slot * p.raw_bytes;
+          for (long long i = b16; i < end; ++i) dst[i - a16] = p.scale[i];
+          mbar_arrive_expect_tx(&raw_full[slot], uint32_t(b16 - a16));
+          if (b16 > a16)
+            bulk_load(smem_u32(dst), p.scale + a16, uint32_t(b16 - a16), &raw_full[slot]);
+          ++it;
+        }
         for (int k = 0; k < nst; ++k) {
           if (!wait_for(p, &empty[stage], phase ^ 1u, &S.abort)) {
             ok = false;
@@ -494,35 +528,15 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
       int zero = 0;
       mbar_wait(&drain[warp], 0, &zero);
     }
-  } else {
-    // ------------------------------------- digits, then epilogue or scales
+  } else if (warp < 12) {
+    // ----------------------------------------------- digits, then epilogue
     const int cw = warp - 4;
-    int stage = 0, it = 0;
-    uint32_t phase = 0;
-    const int row_bytes = p.K / 16;
+    int it = 0;
     for (int ub = u0; ub < u1;) {
       const int pass = ub / blocks;
       const int ue = min(u1, (pass + 1) * blocks);  // this CTA's units of the pass
       const int n_rows = S.pass_n[pass], e = S.pass_e[pass];
       const int16_t* rows = S.sorted + S.pass_at[pass];
-      // warps 8-11: the first scales are under way while the digits are made
-      int lu = ub, lk = 0;  // unit and stage of the next load
-      auto load = [&](uint32_t (&v)[4][4]) {
-        const int first = (min(lu, ue - 1) - pass * blocks) * kUnitRows + lane;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          load_scales<W>(p.scale + ((long long)(e)*p.N + min(first + 32 * c, p.N - 1)) * row_bytes,
-                         lk * 16, row_bytes, v[c]);
-        if (++lk == nst) {
-          lk = 0;
-          lu += 2;
-        }
-      };
-      uint32_t next[kAhead][4][4];
-      if (warp >= 8) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) load(next[i]);
-      }
       {
         // a row's 256-wide blocks over 8, 4, 2 or 1 warps
         const int per = n_rows > 4 ? 1 : n_rows > 2 ? 2 : n_rows > 1 ? 4 : 8;
@@ -655,61 +669,59 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
           if (lane == 0) mbar_arrive(&tempty[it & 1]);
           ++it;
         }
-      } else {
-        // ------------------------------------------------------------ scales
-        // Each warp fills its own lane quarter of TMEM, and every quarter holds
-        // all rows' scales: lane l keeps those of rows l, l + 32, l + 64 and
-        // l + 96, for the next kAhead stages, in registers.
-        const uint32_t quarter = tmem + (uint32_t((cw & 3) * 32) << 16);
-        if (ub == u0) {
-          uint32_t ones[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) ones[i] = 0x38383838u;
-          tmem_st_32x32b_x16(quarter + kColSfb, ones);
-        }
-        const int total = (ue - ub + 1) / 2 * nst;
-        int su = ub, sk = 0;  // unit and stage of the next store
-        for (int q = 0; q < total; q += kAhead) {
-#pragma unroll
-          for (int i = 0; i < kAhead; ++i) {
-            if (q + i >= total) break;
-            // scales are unsigned; none behind K or the tile's last row
-            const int valid = min((su + 1 < ue ? 2 : 1) * kUnitRows,
-                                  p.N - (su - pass * blocks) * kUnitRows);
-            uint32_t v[16];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int left = row_bytes - sk * 16 - 4 * j;  // 2 where K ends inside
-              const uint32_t keep = left >= 4 ? 0x7F7F7F7Fu : left > 0 ? 0x7F7Fu : 0u;
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                v[4 * j + c] = lane + 32 * c < valid ? next[i][c][j] & keep : 0u;
-            }
-            load(next[i]);
-            if (++sk == nst) {
-              sk = 0;
-              su += 2;
-            }
-            wait_for(p, &empty[stage], phase ^ 1u, &S.abort);
-            tc_fence_after();
-            tmem_st_32x32b_x16(quarter + kColSfa + stage * 16, v);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sf_full[stage]);
-            if (++stage == p.stages) {
-              stage = 0;
-              phase ^= 1u;
-            }
-          }
-        }
       }
       ub = ue;
+    }
+  } else {
+    // -------------------------------------------------------------- scales
+    // Each warp fills its own lane quarter of TMEM, and every quarter holds
+    // all rows' scales: lane l writes those of rows l, l + 32, l + 64, l + 96.
+    const uint32_t quarter = tmem + (uint32_t((warp & 3) * 32) << 16);
+    uint32_t v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0x38383838u;  // the tokens' scales: ones
+    tmem_st_32x32b_x16(quarter + kColSfb, v);
+    int stage = 0, it = 0;
+    uint32_t phase = 0;
+    for (int u = u0, two; u < u1; u += two, ++it) {
+      const int pass = u / blocks, block = u - pass * blocks;
+      two = u + 1 < u1 && block + 1 < blocks ? 2 : 1;
+      const int valid = min(two * kUnitRows, p.N - block * kUnitRows);
+      const int slot = it % p.raws;
+      const long long a = ((long long)(S.pass_e[pass]) * p.N + block * kUnitRows) * row_bytes;
+      const uint8_t* rows = raw + slot * p.raw_bytes + int(a & 15) + lane * row_bytes;
+      wait_for(p, &raw_full[slot], (it / p.raws) & 1, &S.abort);
+      for (int k = 0; k < nst; ++k) {
+        uint32_t w[4][4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          load_scales<W>(rows + 32 * c * row_bytes, k * 16, row_bytes, w[c]);
+        // scales are unsigned; none behind K or the tile's last row
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int left = row_bytes - k * 16 - 4 * j;  // 2 where K ends inside
+          const uint32_t keep = left >= 4 ? 0x7F7F7F7Fu : left > 0 ? 0x7F7Fu : 0u;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[4 * j + c] = lane + 32 * c < valid ? w[c][j] & keep : 0u;
+        }
+        wait_for(p, &empty[stage], phase ^ 1u, &S.abort);
+        tc_fence_after();
+        tmem_st_32x32b_x16(quarter + kColSfa + stage * 16, v);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sf_full[stage]);
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (lane == 0) mbar_arrive(&raw_empty[slot]);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kProducer) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -794,6 +806,7 @@ extern "C" moe_status moe_nvfp4_gemv(const void* x, int64_t ldx, int32_t x_per_s
   a.R = num_tokens * top_k;
   a.top_k = top_k;
   a.scale = static_cast<const uint8_t*>(w_scale);
+  a.scale_bytes = (long long)(rows) * (K / 16);
   a.scale2 = w_scale2;
   a.w = static_cast<const uint8_t*>(w);
   a.E = num_experts;
@@ -809,15 +822,23 @@ extern "C" moe_status moe_nvfp4_gemv(const void* x, int64_t ldx, int32_t x_per_s
   a.rp = num_tokens > 2 ? kMaxPassRows : num_tokens;
   const int nst = (K + kStageK - 1) / kStageK;
   const int room = kGemvSmemMax - kGemvStatic - 1024;
-  for (;; a.rp /= 2) {
+  a.raw_bytes = 128 * (K / 16) + 32;
+  a.raws = 2;
+  for (;;) {
     a.xrows = a.rp * kDigits < 16 ? 16 : a.rp * kDigits;
-    a.stages = (room - nst * a.xrows * 128) / kStageBytes;
-    if (a.stages >= 4 || a.rp == 1) break;
+    a.stages = (room - nst * a.xrows * 128 - a.raws * a.raw_bytes) / kStageBytes;
+    if (a.stages >= 4) break;
+    if (a.raws == 2)
+      a.raws = 1;
+    else if (a.rp > 2)
+      a.rp /= 2;
+    else
+      break;
   }
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   const long long most = (long long)(a.R) * ((N + kUnitRows - 1) / kUnitRows);
   const int grid = int(most < sms ? most : sms);
-  const int smem = 1024 + a.stages * kStageBytes + nst * a.xrows * 128;
+  const int smem = 1024 + a.stages * kStageBytes + nst * a.xrows * 128 + a.raws * a.raw_bytes;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == MOE_DTYPE_BF16;
   const int row_bytes = K / 16;  // of scales: even
