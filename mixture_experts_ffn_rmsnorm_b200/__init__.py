@@ -176,32 +176,32 @@ def _launch_stream(what, stream, *tensors) -> Optional[int]:
 
 def _rows_ld(t, what, name) -> int:
     """Leading dimension of a row tensor [rows, width] (unit stride along a row)."""
-    if t.dim() != 2:
+    st = t.stride()
+    if len(st) != 2:
         raise MoEError(1, f"{what}: {name} is not two-dimensional")
     rows, width = t.shape
-    if width > 1 and rows > 0 and t.stride(1) != 1:
+    if st[1] != 1 and width > 1 and rows > 0:
         raise MoEError(1, f"{what}: {name}'s rows are not contiguous")
-    return t.stride(0) if rows > 1 else (width + 7) // 8 * 8
+    return st[0] if rows > 1 else (width + 7) // 8 * 8
 
 
 def _experts_ld(t, what, name) -> int:
     """Leading dimension of stacked matrices [E, N, K]: matrices back to back."""
-    if t.dim() != 3:
+    st = t.stride()
+    if len(st) != 3:
         raise MoEError(1, f"{what}: {name} is not three-dimensional")
     E, N, K = t.shape
-    if K > 1 and t.stride(2) != 1:
+    if st[2] != 1 and K > 1:
         raise MoEError(1, f"{what}: {name}'s rows are not contiguous")
     if N > 1:
-        ld = t.stride(1)
-        if E > 1 and t.stride(0) != N * ld:
+        if E > 1 and st[0] != N * st[1]:
             raise MoEError(1, f"{what}: {name}'s matrices do not lie back to back")
-        return ld
-    return t.stride(0) if E > 1 else (K + 7) // 8 * 8
+        return st[1]
+    return st[0] if E > 1 else (K + 7) // 8 * 8
 
 
 def _check_off(off, E, what):
-    if off.dtype != _torch.int32 or off.dim() != 1 or off.shape[0] != E + 1 or (
-            not off.is_contiguous()):
+    if off.dtype != _torch.int32 or off.shape != (E + 1,) or not off.is_contiguous():
         raise MoEError(1, f"{what}: off is not a contiguous int32 tensor [num_experts + 1]")
 
 
@@ -219,7 +219,7 @@ def grouped_gemm(x, w, off, y, relu2=False, status=None, stream=None):
     int32.  Rows outside every group are left as they are.  relu2 applies
     max(v, 0)^2.  status: optional int32 word the device ORs error bits into."""
     what = "moe_grouped_gemm"
-    _need_torch()
+    _torch or _need_torch()
     ldx, ldw, ldy = _rows_ld(x, what, "x"), _experts_ld(w, what, "w"), _rows_ld(y, what, "y")
     E, N, K = w.shape
     rows = x.shape[0]
@@ -231,8 +231,9 @@ def grouped_gemm(x, w, off, y, relu2=False, status=None, stream=None):
     _check_off(off, E, what)
     _check_status(status, what)
     s = _launch_stream(what, stream, x, w, off, y, status)
-    st = (_lib or load_library()).moe_grouped_gemm(_ptr(x), ldx, _ptr(w), ldw, _ptr(off), E, rows, K, N, dt,
-                                         int(relu2), _ptr(y), ldy, _ptr(status), s)
+    st = (_lib or load_library()).moe_grouped_gemm(
+        x.data_ptr(), ldx, w.data_ptr(), ldw, off.data_ptr(), E, rows, K, N, dt, int(relu2),
+        y.data_ptr(), ldy, _ptr(status), s)
     if st != 0:
         raise MoEError(st, what)
 
@@ -243,7 +244,7 @@ def grouped_gemm_dgrad(dy, w, off, dx, status=None, stream=None):
 
     dy [rows, N], w [E, N, K], dx [rows, K]; the rest as in grouped_gemm."""
     what = "moe_grouped_gemm_dgrad"
-    _need_torch()
+    _torch or _need_torch()
     ldy, ldw, ldx = _rows_ld(dy, what, "dy"), _experts_ld(w, what, "w"), _rows_ld(dx, what, "dx")
     E, N, K = w.shape
     rows = dy.shape[0]
@@ -255,8 +256,9 @@ def grouped_gemm_dgrad(dy, w, off, dx, status=None, stream=None):
     _check_off(off, E, what)
     _check_status(status, what)
     s = _launch_stream(what, stream, dy, w, off, dx, status)
-    st = (_lib or load_library()).moe_grouped_gemm_dgrad(_ptr(dy), ldy, _ptr(w), ldw, _ptr(off), E, rows, K,
-                                               N, dt, _ptr(dx), ldx, _ptr(status), s)
+    st = (_lib or load_library()).moe_grouped_gemm_dgrad(
+        dy.data_ptr(), ldy, w.data_ptr(), ldw, off.data_ptr(), E, rows, K, N, dt, dx.data_ptr(),
+        ldx, _ptr(status), s)
     if st != 0:
         raise MoEError(st, what)
 
@@ -269,7 +271,7 @@ def grouped_gemm_wgrad(dy, x, off, dw, accumulate=False, status=None, stream=Non
     dy [rows, N], x [rows, K]; dw [E, N, K] of the same dtype or float32.
     accumulate (float32 only) adds to dw.  The rest as in grouped_gemm."""
     what = "moe_grouped_gemm_wgrad"
-    _need_torch()
+    _torch or _need_torch()
     ldy, ldx, ldw = _rows_ld(dy, what, "dy"), _rows_ld(x, what, "x"), _experts_ld(dw, what, "dw")
     E, N, K = dw.shape
     rows = dy.shape[0]
@@ -281,9 +283,9 @@ def grouped_gemm_wgrad(dy, x, off, dw, accumulate=False, status=None, stream=Non
     _check_off(off, E, what)
     _check_status(status, what)
     s = _launch_stream(what, stream, dy, x, off, dw, status)
-    st = (_lib or load_library()).moe_grouped_gemm_wgrad(_ptr(dy), ldy, _ptr(x), ldx, _ptr(off), E, rows, K,
-                                               N, dt, _ptr(dw), ldw, _dtype_code(dw, what),
-                                               int(accumulate), _ptr(status), s)
+    st = (_lib or load_library()).moe_grouped_gemm_wgrad(
+        dy.data_ptr(), ldy, x.data_ptr(), ldx, off.data_ptr(), E, rows, K, N, dt, dw.data_ptr(),
+        ldw, _dtype_code(dw, what), int(accumulate), _ptr(status), s)
     if st != 0:
         raise MoEError(st, what)
 
@@ -298,7 +300,7 @@ def nvfp4_gemv(x, idx, w, w_scale, w_scale2, y, relu2=False, status=None, stream
     y [T, k, N] of x's dtype.  relu2 applies max(v, 0)^2.  An id outside
     [0, E) gives a zero row and bit 2 of status."""
     what = "moe_nvfp4_gemv"
-    torch = _need_torch()
+    torch = _torch or _need_torch()
     if idx.dim() != 2 or idx.dtype != torch.int32 or not idx.is_contiguous():
         raise MoEError(1, f"{what}: idx is not a contiguous int32 tensor [T, k]")
     T, k = idx.shape
@@ -322,9 +324,9 @@ def nvfp4_gemv(x, idx, w, w_scale, w_scale2, y, relu2=False, status=None, stream
     ldy = _experts_ld(y, what, "y")
     _check_status(status, what)
     s = _launch_stream(what, stream, x, idx, w, w_scale, w_scale2, y, status)
-    st = (_lib or load_library()).moe_nvfp4_gemv(_ptr(x), ldx, int(per_slot), _ptr(idx), T, k, _ptr(w),
-                                       _ptr(w_scale), _ptr(w_scale2), E, K, N, dt, int(relu2),
-                                       _ptr(y), ldy, _ptr(status), s)
+    st = (_lib or load_library()).moe_nvfp4_gemv(
+        x.data_ptr(), ldx, int(per_slot), idx.data_ptr(), T, k, w.data_ptr(), w_scale.data_ptr(),
+        w_scale2.data_ptr(), E, K, N, dt, int(relu2), y.data_ptr(), ldy, _ptr(status), s)
     if st != 0:
         raise MoEError(st, what)
 

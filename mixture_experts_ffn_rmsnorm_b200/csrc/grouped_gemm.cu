@@ -338,37 +338,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      while (ok && walk.next(p, s_rows, s_pre, rgroup)) {
-        const GTile& t = walk.t;
-        const int nmma = (t.nr + 15) & ~15;
-        const int nb = nmma / CG;  // r's of B this CTA loads
-        const int ca = t.c0 + int(rank) * 128;
-        const int rb = t.r0 + int(rank) * nb;
-        // B of one k-block: one K-major box of 16, 32, 64 or 128 rows (several
-        // smaller ones cost more than the rows they save), or MN-major boxes
-        // of 64
-        int nbox = 1, size = 0;
-        uint32_t bbytes;
-        if (Tr::kBMN) {
-          nbox = (nb + 63) / 64;
-          bbytes = nbox * 64 * 128;
-        } else {
-          size = nb <= 16 ? 0 : nb <= 32 ? 1 : nb <= 64 ? 2 : 3;
-          bbytes = 2048u << size;
-        }
-        for (int kb0 = 0; kb0 < t.nk; kb0 += KPS) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort)) {
-            give_up(p, abort);
-            ok = false;
-            break;
-          }
-          const int kbn = min(KPS, t.nk - kb0);
-          const uint32_t bytes = uint32_t(kbn) * (Tr::kABytes + bbytes);
-          const bool is_tail = M == kWgrad && kb0 + 1 == t.nk && (t.cnt & (kBK - 1)) != 0;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    while (ok && uniform(walk.next(p, s_rows, s_pre, rgroup))) {
+      const int nk = uniform(walk.t.nk), nr = uniform(walk.t.nr), cnt = uniform(walk.t.cnt);
+      const int e = uniform(walk.t.e), row0 = uniform(walk.t.row0), r0 = uniform(walk.t.r0);
+      const int nmma = (nr + 15) & ~15;
+      const int nb = nmma / CG;  // r's of B this CTA loads
+      const int ca = uniform(walk.t.c0) + int(rank) * 128;
+      const int rb = r0 + int(rank) * nb;
+      // B of one k-block: one K-major box of 16, 32, 64 or 128 rows (several
+      // smaller ones cost more than the rows they save), or MN-major boxes
+      // of 64
+      int nbox = 1, size = 0;
+      uint32_t bbytes;
+      if (Tr::kBMN) {
+        nbox = (nb + 63) / 64;
+        bbytes = nbox * 64 * 128;
+      } else {
+        size = nb <= 16 ? 0 : nb <= 32 ? 1 : nb <= 64 ? 2 : 3;
+        bbytes = 2048u << size;
+      }
+      for (int kb0 = 0; kb0 < nk; kb0 += KPS) {
+        ok = uniform(mbar_wait(&empty[stage], phase ^ 1u, abort));
+        if (!ok) break;
+        const int kbn = min(KPS, nk - kb0);
+        const uint32_t bytes = uint32_t(kbn) * (Tr::kABytes + bbytes);
+        const bool is_tail = M == kWgrad && kb0 + 1 == nk && (cnt & (kBK - 1)) != 0;
+        const uint32_t st = tiles_u32 + stage * Tr::kStageBytes;
+        if (elect_one()) {
           uint32_t bar;
           if (is_tail) {
             mbar_arrive_expect_tx(&tail[stage], bytes);
@@ -380,94 +379,101 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(&full[stage], bytes);
             bar = smem_u32(&full[stage]);
           }
-          for (int kk = 0; kk < kbn; ++kk) {
-            const int kb = kb0 + kk;
-            const uint32_t sa = tiles_u32 + stage * Tr::kStageBytes + kk * (Tr::kABytes + Tr::kBBytes);
-            const uint32_t sb = sa + Tr::kABytes;
-            if constexpr (M == kFwd) {
-              tma_load_3d<CG>(sa, &p.tmA, bar, kb * kBK, ca, t.e);
-            } else {
-              const int y = M == kDgrad ? kb * kBK : t.row0 + kb * kBK;
-              const int z = M == kDgrad ? t.e : 0;
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                tma_load_3d<CG>(sa + h * 8192, &p.tmA, bar, ca + h * 64, y, z);
+          for (int kk = 0; kk < KPS; ++kk) {
+            if (kk >= kbn) break;
+            const int q = (kb0 + kk) * kBK;
+            const uint32_t sa = st + kk * (Tr::kABytes + Tr::kBBytes), sb = sa + Tr::kABytes;
+            if constexpr (M == kFwd) {
+              tma_load_3d<CG>(sa, &p.tmA, bar, q, ca, e);
+            } else {
+              const int y = M == kDgrad ? q : row0 + q;
+              const int z = M == kDgrad ? e : 0;
+              tma_load_3d<CG>(sa, &p.tmA, bar, ca, y, z);
+              tma_load_3d<CG>(sa + 8192, &p.tmA, bar, ca + 64, y, z);
             }
             if constexpr (M == kWgrad) {
               for (int h = 0; h < nbox; ++h)
-                tma_load_3d<CG>(sb + h * 8192, &p.tmB[0], bar, rb + h * 64, t.row0 + kb * kBK, 0);
+                tma_load_3d<CG>(sb + h * 8192, &p.tmB[0], bar, rb + h * 64, row0 + q, 0);
             } else {
-              tma_load_3d<CG>(sb, &p.tmB[size], bar, kb * kBK, t.row0 + rb, 0);
+              tma_load_3d<CG>(sb, &p.tmB[size], bar, q, row0 + rb, 0);
             }
           }
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok) {  // let the copies in flight land before the CTA may exit
-        const long long t0 = clock64();
-        while (clock64() - t0 < 4000000) {
-        }
+    }
+    if (!ok) {
+      if (lane == 0) give_up(p, abort);
+      const long long t0 = clock64();  // let the copies in flight land before the CTA may exit
+      while (clock64() - t0 < 4000000) {
       }
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0 && rank == 0) {
+    // The whole warp walks the tiles with warp-uniform values and one lane
+    // issues: from a single lane's divergent branch each tcgen05.mma took
+    // about 180 cycles to issue, more than the 128 of its 256 x 256 x 16
+    // product.
+    if (rank == 0) {
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true;
-      while (ok && walk.next(p, s_rows, s_pre, rgroup)) {
-        const GTile& t = walk.t;
-        if (t.nk == 0) continue;
-        const int nmma = (t.nr + 15) & ~15;
-        const uint32_t idesc = make_idesc_16(128 * CG, nmma, p.fmt, Tr::kAMN, Tr::kBMN);
+      while (ok && uniform(walk.next(p, s_rows, s_pre, rgroup))) {
+        const int nk = uniform(walk.t.nk), nr = uniform(walk.t.nr), cnt = uniform(walk.t.cnt);
+        if (nk == 0) continue;
+        const uint32_t idesc = make_idesc_16(128 * CG, (nr + 15) & ~15, p.fmt, Tr::kAMN, Tr::kBMN);
         const int ab = it & 1;
-        if (!mbar_wait(&tempty[ab], ((it >> 1) & 1) ^ 1u, abort)) {
-          give_up(p, abort);
-          break;
-        }
+        ok = uniform(mbar_wait(&tempty[ab], ((it >> 1) & 1) ^ 1u, abort));
+        if (!ok) break;
         ++it;
         tc_fence_after();
         const uint32_t d = tmem_base + uint32_t(ab * NB);
-        for (int kb0 = 0; kb0 < t.nk; kb0 += KPS) {
+        const int last = (cnt - (nk - 1) * kBK + 15) / 16;  // weight gradient: steps with rows
+        for (int kb0 = 0; kb0 < nk; kb0 += KPS) {
           // a group's last k-block: the pair's warps 2 may have written to it
-          const bool is_tail = M == kWgrad && kb0 + 1 == t.nk && (t.cnt & (kBK - 1)) != 0;
-          if (!(CG == 2 && is_tail ? mbar_wait_acquire_cluster(&full[stage], phase, abort)
-                                   : mbar_wait(&full[stage], phase, abort))) {
-            give_up(p, abort);
-            ok = false;
-            break;
-          }
+          const bool is_tail = M == kWgrad && kb0 + 1 == nk && (cnt & (kBK - 1)) != 0;
+          ok = uniform(CG == 2 && is_tail ? mbar_wait_acquire_cluster(&full[stage], phase, abort)
+                                          : mbar_wait(&full[stage], phase, abort));
+          if (!ok) break;
           tc_fence_after();
-          const int kbn = min(KPS, t.nk - kb0);
-          for (int kk = 0; kk < kbn; ++kk) {
-            const uint32_t sa = tiles_u32 + stage * Tr::kStageBytes + kk * (Tr::kABytes + Tr::kBBytes);
-            const uint32_t sb = sa + Tr::kABytes;
-            const uint64_t ad = Tr::kAMN ? smem_desc_mn_sw128(sa, 8192)
-                                         : smem_desc_sw128(tiles + (sa - tiles_u32));
-            const uint64_t bd = Tr::kBMN ? smem_desc_mn_sw128(sb, 8192)
-                                         : smem_desc_sw128(tiles + (sb - tiles_u32));
-            int ks = kBK / 16;
-            if (M == kWgrad && kb0 + kk + 1 == t.nk)
-              ks = (t.cnt - (t.nk - 1) * kBK + 15) / 16;  // only the steps with rows
+          const int kbn = min(KPS, nk - kb0);
+          const uint32_t sa0 = tiles_u32 + stage * Tr::kStageBytes;
+          if (elect_one()) {
 #pragma unroll
-            for (int s = 0; s < kBK / 16; ++s)
-              if (s < ks)
-                umma_f16_cg<CG>(d, ad + s * (Tr::kAMN ? 128 : 2), bd + s * (Tr::kBMN ? 128 : 2),
-                                idesc, (kb0 | kk | s) ? 1u : 0u);
+            for (int kk = 0; kk < KPS; ++kk) {
+              if (kk >= kbn) break;
+              const uint32_t sa = sa0 + kk * (Tr::kABytes + Tr::kBBytes), sb = sa + Tr::kABytes;
+              const uint64_t ad =
+                  Tr::kAMN ? smem_desc_mn_sw128(sa, 8192) : smem_desc_k_sw128(sa);
+              const uint64_t bd =
+                  Tr::kBMN ? smem_desc_mn_sw128(sb, 8192) : smem_desc_k_sw128(sb);
+              const int ks = M == kWgrad && kb0 + 1 == nk ? last : kBK / 16;
+#pragma unroll
+              for (int s = 0; s < kBK / 16; ++s)
+                if (M != kWgrad || s < ks)
+                  umma_f16_cg<CG>(d, ad + s * (Tr::kAMN ? 128 : 2), bd + s * (Tr::kBMN ? 128 : 2),
+                                  idesc, (kb0 | kk | s) ? 1u : 0u);
+            }
+            umma_commit_cg<CG>(&empty[stage]);
           }
-          umma_commit_cg<CG>(&empty[stage]);
+          __syncwarp();
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (ok) umma_commit_cg<CG>(&tfull[ab]);
+        if (ok && elect_one()) umma_commit_cg<CG>(&tfull[ab]);
+        __syncwarp();
       }
+      if (!ok && lane == 0) give_up(p, abort);
       // every MMA issued has completed once `drain` flips (in both CTAs)
-      umma_commit_cg<CG>(drain);
+      if (elect_one()) umma_commit_cg<CG>(drain);
+      __syncwarp();
       int zero = 0;
       mbar_wait(drain, 0, &zero);
     }
@@ -529,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the bulk store of the chunk before has read the staging tile
         const bool bulk = M == kWgrad && p.tma_out;
         if (bulk) {
-          if (lane == 0) bulk_wait_read();
+          if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
         }
         if constexpr (EB == 4) {

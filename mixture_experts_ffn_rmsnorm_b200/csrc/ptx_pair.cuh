@@ -13,6 +13,25 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
+// The value of lane 0, for the whole warp: the compiler then knows it to be
+// warp-uniform and keeps what follows from it in uniform registers, where the
+// tensor-core instructions want their operands.
+template <class T>
+__device__ __forceinline__ T uniform(T v) {
+  return T(__shfl_sync(0xffffffffu, v, 0));
+}
+
 // Barrier over all threads of the cluster; orders shared-memory accesses.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -101,8 +120,9 @@ __device__ __forceinline__ void bulk_commit() {
 
 // Wait until this thread's bulk groups have read their shared memory / are
 // complete.
+template <int PENDING>  // but the last PENDING ones
 __device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(PENDING) : "memory");
 }
 __device__ __forceinline__ void bulk_wait_all() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -213,6 +233,17 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t tile, uint32_t b
   uint64_t d = 0;
   d |= uint64_t((tile >> 4) & 0x3FFFu);
   d |= uint64_t((block_bytes >> 4) & 0x3FFFu) << 16;
+  d |= uint64_t(1024 >> 4) << 32;
+  d |= uint64_t(1) << 46;  // version
+  d |= uint64_t(2) << 61;  // SWIZZLE_128B
+  return d;
+}
+
+// smem_desc_sw128 (K-major, 128-byte swizzle) from a shared address.
+__device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t tile) {
+  uint64_t d = 0;
+  d |= uint64_t((tile >> 4) & 0x3FFFu);
+  d |= uint64_t(1) << 16;
   d |= uint64_t(1024 >> 4) << 32;
   d |= uint64_t(1) << 46;  // version
   d |= uint64_t(2) << 61;  // SWIZZLE_128B
