@@ -63,7 +63,6 @@ struct GroupedArgs {
   long long group_stride;  // elements (weight gradient)
   uint32_t fmt;            // 0 = FP16, 1 = BF16
   int relu2;
-  int rgroup;  // r tiles of a unit (forward, data gradient)
   int accumulate;  // out += (FP32 only)
   int tma_out;     // weight gradient: whole chunks leave by TMA
   int vec;         // 16-byte stores: base, ldo and group_stride allow them
@@ -97,43 +96,52 @@ struct GTile {
   int nk;    // k-blocks
 };
 
-// The tiles of one CTA (pair), in order.  Work is handed out in units: one c
-// tile with up to `rgroup` r tiles of a group after one another, so that the
-// second finds the weights that the first brought in in L2.  Unit u goes to
-// CTA (pair) u mod step; pre[e] = units of the groups before e.
+// The tiles of one CTA (pair), in order.  Tile number u of the launch is c tile
+// u % ct of row tile u / ct, row tiles counted over all groups (pre[e] = row
+// tiles of the groups before e); CTA (pair) i takes the tiles i, i + step, ...
+// The quotient and the remainder are carried along, so that the next tile
+// costs a few additions (with a division, and the group's bounds read again,
+// the roles spent 1400 cycles a tile on it, more than on a tile of one k-block).
 template <Mode M, int TILE_C, int NB>
 struct Walk {
-  int u, step, e = 0, more = 0;
+  int ct, step_q, step_r;
+  int q, r;         // row tile and c tile of the next tile
+  int e = 0, lo = 0, hi;  // current group and its row tiles
   GTile t;
 
-  __device__ __forceinline__ Walk(int first, int step_) : u(first), step(step_) {}
-
-  __device__ __forceinline__ bool next(const GroupedArgs& p, const int* off, const int* pre,
-                                       int rgroup) {
-    if (more > 0) {
-      --more;
-      t.r0 += NB;
-    } else {
-      if (u >= pre[p.groups]) return false;
-      while (pre[e + 1] <= u) ++e;
-      const int ct = (p.C + TILE_C - 1) / TILE_C;
-      const int i = u - pre[e];
-      const int rg = i / ct;
-      t.e = e;
-      t.row0 = off[2 * e];
-      t.cnt = off[2 * e + 1];
-      t.c0 = (i - rg * ct) * TILE_C;
-      t.r0 = rg * rgroup * NB;
-      t.nk = ((M == kWgrad ? t.cnt : p.Q) + kBK - 1) / kBK;
-      const int left = (ext(p) - t.r0 + NB - 1) / NB;
-      more = min(rgroup, left) - 1;
-      u += step;
-    }
-    t.nr = min(NB, ext(p) - t.r0);
-    return true;
+  __device__ __forceinline__ Walk(const GroupedArgs& p, const int* off, const int* pre, int first,
+                                  int step)
+      : ct((p.C + TILE_C - 1) / TILE_C), step_q(step / ct), step_r(step % ct), q(first / ct),
+        r(first % ct), hi(pre[1]) {
+    group(p, off, 0);
   }
-  __device__ __forceinline__ int ext(const GroupedArgs& p) const {
-    return M == kWgrad ? p.R : t.cnt;
+
+  __device__ __forceinline__ void group(const GroupedArgs& p, const int* off, int g) {
+    t.e = g;
+    t.row0 = off[2 * g];
+    t.cnt = off[2 * g + 1];
+    t.nk = ((M == kWgrad ? t.cnt : p.Q) + kBK - 1) / kBK;
+  }
+
+  __device__ __forceinline__ bool next(const GroupedArgs& p, const int* off, const int* pre) {
+    if (q >= hi) {
+      do {
+        if (++e >= p.groups) return false;
+        lo = hi;
+        hi = pre[e + 1];
+      } while (q >= hi);
+      group(p, off, e);
+    }
+    t.c0 = r * TILE_C;
+    t.r0 = (q - lo) * NB;
+    t.nr = min(NB, (M == kWgrad ? p.R : t.cnt) - t.r0);
+    q += step_q;
+    r += step_r;
+    if (r >= ct) {
+      r -= ct;
+      ++q;
+    }
+    return true;
   }
 };
 
@@ -298,10 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, Tr::kTmemCols);
 
-  // the work list: units of each group, prefix sums
-  const int rgroup = M == kWgrad ? 1 : p.rgroup;
+  // the work list: row tiles of each group, prefix sums
   {
-    const int ct = (p.C + Tr::kTileC - 1) / Tr::kTileC;
     const int e = threadIdx.x;
     int n = 0;
     if (e < p.groups) {
@@ -311,8 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cnt = good ? b - a : 0;
       s_rows[2 * e] = good ? a : 0;
       s_rows[2 * e + 1] = cnt;
-      const int rt = ((M == kWgrad ? p.R : cnt) + NB - 1) / NB;
-      n = (rt + rgroup - 1) / rgroup * ct;
+      n = ((M == kWgrad ? p.R : cnt) + NB - 1) / NB;
       if (M == kWgrad && cnt == 0 && p.accumulate) n = 0;  // nothing to add
       if (M == kWgrad && !good) n = 0;  // a bad group's gradient is left as it was
     }
@@ -333,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  Walk<M, Tr::kTileC, NB> walk(int(blockIdx.x) / CG, int(gridDim.x) / CG);
+  Walk<M, Tr::kTileC, NB> walk(p, s_rows, s_pre, int(blockIdx.x) / CG, int(gridDim.x) / CG);
   const uint32_t tiles_u32 = smem_u32(tiles);
 
   if (warp == 0) {
@@ -341,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    while (ok && uniform(walk.next(p, s_rows, s_pre, rgroup))) {
+    while (ok && uniform(walk.next(p, s_rows, s_pre))) {
       const int nk = uniform(walk.t.nk), nr = uniform(walk.t.nr), cnt = uniform(walk.t.cnt);
       const int e = uniform(walk.t.e), row0 = uniform(walk.t.row0), r0 = uniform(walk.t.r0);
       const int nmma = (nr + 15) & ~15;
@@ -423,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true;
-      while (ok && uniform(walk.next(p, s_rows, s_pre, rgroup))) {
+      while (ok && uniform(walk.next(p, s_rows, s_pre))) {
         const int nk = uniform(walk.t.nk), nr = uniform(walk.t.nr), cnt = uniform(walk.t.cnt);
         if (nk == 0) continue;
         const uint32_t idesc = make_idesc_16(128 * CG, (nr + 15) & ~15, p.fmt, Tr::kAMN, Tr::kBMN);
@@ -481,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------- rows behind a group's last one
     int total = 0;
     uint32_t used = 0;  // phase bit of each stage's tail barrier
-    while (walk.next(p, s_rows, s_pre, rgroup)) {
+    while (walk.next(p, s_rows, s_pre)) {
       const GTile& t = walk.t;
       total += t.nk;
       const int valid = t.cnt & (kBK - 1);
@@ -514,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = (warp - 4) >> 2;  // chunks of 32 r's: even or odd ones
     const uint32_t st = smem_u32(staging) + (warp - 4) * Tr::kWarpStaging;
     int it = 0;
-    while (walk.next(p, s_rows, s_pre, rgroup)) {
+    while (walk.next(p, s_rows, s_pre)) {
       const GTile& t = walk.t;
       const int cw = t.c0 + int(rank) * 128 + q * 32;
       const long long row = M == kWgrad ? t.r0 : (long long)(t.row0) + t.r0;
@@ -708,7 +713,6 @@ moe_status dispatch(GroupedArgs& a, const Operand& A, const Operand& B, bool out
   const moe_status st = current_device(&dev, &sms);
   if (st != MOE_OK) return st;
   if constexpr (M != kWgrad) {
-    a.rgroup = 1;
     if (a.rows <= 64LL * a.groups) return run_variant<M, 1, 64, 2, 4, 2>(a, A, B, dev, sms, stream);
     if (a.rows <= 128LL * a.groups)
       return run_variant<M, 2, 128, 2, 4, 2>(a, A, B, dev, sms, stream);
