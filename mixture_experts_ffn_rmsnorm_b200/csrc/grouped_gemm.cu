@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int s_scan[kThreads / 32];
   __shared__ int s_rows[2 * MOE_MAX_EXPERTS];  // {first row, rows} of each group
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = uniform(int(threadIdx.x >> 5));
   const int lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
 
@@ -519,15 +519,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = (warp - 4) >> 2;  // chunks of 32 r's: even or odd ones
     const uint32_t st = smem_u32(staging) + (warp - 4) * Tr::kWarpStaging;
     int it = 0;
-    while (walk.next(p, s_rows, s_pre)) {
-      const GTile& t = walk.t;
-      const int cw = t.c0 + int(rank) * 128 + q * 32;
-      const long long row = M == kWgrad ? t.r0 : (long long)(t.row0) + t.r0;
-      const long long base = (M == kWgrad ? t.e * p.group_stride : 0) + row * p.ldo;
+    while (uniform(walk.next(p, s_rows, s_pre))) {
+      const int nk = uniform(walk.t.nk), nr = uniform(walk.t.nr), r0 = uniform(walk.t.r0);
+      const int e = uniform(walk.t.e);
+      const int cw = uniform(walk.t.c0) + int(rank) * 128 + q * 32;
+      const long long row = M == kWgrad ? r0 : (long long)(uniform(walk.t.row0)) + r0;
+      const long long base = (M == kWgrad ? e * p.group_stride : 0) + row * p.ldo;
       const int ab = it & 1;
-      if (t.nk > 0) {
-        if (!mbar_wait(&tfull[ab], (it >> 1) & 1, abort)) {
-          give_up(p, abort);
+      if (nk > 0) {
+        if (!uniform(mbar_wait(&tfull[ab], (it >> 1) & 1, abort))) {
+          if (lane == 0) give_up(p, abort);
           break;
         }
         ++it;
@@ -536,16 +537,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tb = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(ab * NB);
       const bool mine = cw < p.C;  // the warp has c's to store
 #pragma unroll 1
-      for (int j0 = half * 32; j0 < t.nr && mine; j0 += 64) {
+      for (int j0 = half * 32; j0 < nr && mine; j0 += 64) {
         // the bulk store of the chunk before has read the staging tile
         const bool bulk = M == kWgrad && p.tma_out;
         if (bulk) {
-          if (lane == 0) bulk_wait_read<0>();
+          if (elect_one()) bulk_wait_read<0>();
           __syncwarp();
         }
         if constexpr (EB == 4) {
           uint32_t r[32];
-          if (t.nk > 0) {
+          if (nk > 0) {
             tmem_ld_32x32b_x32(tb + uint32_t(j0), r);
             tmem_ld_wait();
           } else {  // an empty group's gradient
@@ -556,10 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             stage_chunk_32(r, st);
           else if (cw + lane < p.C)
             store_chunk_32(p, r, static_cast<float*>(p.out) + base + j0 * p.ldo + cw + lane,
-                           t.nr - j0);
+                           nr - j0);
         } else {
           uint32_t r[2][16];
-          if (t.nk > 0) {
+          if (nk > 0) {
             tmem_ld_16x256b_x4(tb + uint32_t(j0), r[0]);
             tmem_ld_16x256b_x4(tb + (16u << 16) + uint32_t(j0), r[1]);
             tmem_ld_wait_regs(r);
@@ -571,20 +572,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!bulk) {
             __syncwarp();
             store_chunk_16(p, st, static_cast<uint16_t*>(p.out) + base + j0 * p.ldo, cw,
-                           t.nr - j0);
+                           nr - j0);
             __syncwarp();
           }
         }
         if (bulk) {
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            tma_store_3d(&p.tmO, st, cw, t.r0 + j0, t.e);
+          if (elect_one()) {
+            tma_store_3d(&p.tmO, st, cw, r0 + j0, e);
             bulk_commit();
           }
         }
       }
-      if (t.nk > 0) {
+      if (nk > 0) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -595,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (M == kWgrad && lane == 0) bulk_wait_all();
+    if (M == kWgrad && elect_one()) bulk_wait_all();
   }
 
   tc_fence_before();
