@@ -51,7 +51,7 @@ constexpr int kBK = 64;        // elements of q per k-block (128 bytes)
 struct GroupedArgs {
   CUtensorMap tmA;     // forward: 128-row boxes; else 64-row boxes
   CUtensorMap tmB[4];  // K-major: boxes of 16, 32, 64 and 128 rows; weight gradient: [0], 64
-  CUtensorMap tmO;     // weight gradient with `tma_out`: 32 x 32 boxes of the output
+  CUtensorMap tmO;     // weight gradient with `tma_out`: a round's 32 or 64 r's x 32 c's of the output
   const int* off;
   int groups;
   int rows;  // rows of the row tensors: no group may end behind it
@@ -78,7 +78,11 @@ struct Traits {
   static constexpr int kStageBytes = KPS * (kABytes + kBBytes);
   static constexpr int kTileC = 128 * CG;
   static constexpr int kTmemCols = 2 * NB;
-  static constexpr int kWarpStaging = 32 * 32 * EB;  // one chunk of the epilogue
+  static constexpr int kChunk = 32 * 32 * EB;  // 32 r's x 32 c's of the epilogue
+  // chunks a warp stores at a time: each round waits for its staging tile,
+  // fences it and issues one copy, 340 cycles of a chunk's 620
+  static constexpr int kRound = M == kWgrad && EB == 2 ? 2 : 1;
+  static constexpr int kWarpStaging = kRound * kChunk;
   static constexpr int kStagingBytes = kEpiWarps * kWarpStaging;
   static constexpr int kSmem = 1024 + STAGES * kStageBytes + kStagingBytes + 512;
   static_assert(!kBMN || KPS == 1, "the tail of a group is one k-block of one stage");
@@ -177,27 +181,29 @@ __device__ __forceinline__ uint32_t staging_at(uint32_t r, uint32_t b) {
 // transposing stmatrix leaves rows of 32 c's in shared memory, which go out
 // as 16-byte stores.  Measured against one 2-byte store per element and
 // lane into the staging tile: wgrad at 48 rows a group 655 -> see below.
-__device__ __forceinline__ void stage_chunk_16(const GroupedArgs& p, uint32_t (&acc)[2][16],
-                                               uint32_t staging) {
+__device__ __forceinline__ void stage_chunk_16(const GroupedArgs& p, uint32_t (&lo)[16],
+                                               uint32_t (&hi)[16], uint32_t staging) {
   const uint32_t lane = threadIdx.x & 31;
   if (p.relu2) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        acc[h][j] = __float_as_uint(relu2(__uint_as_float(acc[h][j])));
+    for (int j = 0; j < 16; ++j) {
+      lo[j] = __float_as_uint(relu2(__uint_as_float(lo[j])));
+      hi[j] = __float_as_uint(relu2(__uint_as_float(hi[j])));
+    }
   }
   uint32_t m[2][8];
   if (p.fmt) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m[h][j] = pack_16(acc[h][2 * j], acc[h][2 * j + 1], true);
+    for (int j = 0; j < 8; ++j) {
+      m[0][j] = pack_16(lo[2 * j], lo[2 * j + 1], true);
+      m[1][j] = pack_16(hi[2 * j], hi[2 * j + 1], true);
+    }
   } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m[h][j] = pack_16(acc[h][2 * j], acc[h][2 * j + 1], false);
+    for (int j = 0; j < 8; ++j) {
+      m[0][j] = pack_16(lo[2 * j], lo[2 * j + 1], false);
+      m[1][j] = pack_16(hi[2 * j], hi[2 * j + 1], false);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -537,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tb = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(ab * NB);
       const bool mine = cw < p.C;  // the warp has c's to store
 #pragma unroll 1
-      for (int j0 = half * 32; j0 < nr && mine; j0 += 64) {
-        // the bulk store of the chunk before has read the staging tile
+      for (int j0 = half * 32 * Tr::kRound; j0 < nr && mine; j0 += 64 * Tr::kRound) {
+        // the bulk store of the round before has read the staging tile
         const bool bulk = M == kWgrad && p.tma_out;
         if (bulk) {
           if (elect_one()) bulk_wait_read<0>();
@@ -559,20 +565,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             store_chunk_32(p, r, static_cast<float*>(p.out) + base + j0 * p.ldo + cw + lane,
                            nr - j0);
         } else {
-          uint32_t r[2][16];
+          uint32_t r[2 * Tr::kRound][16];
           if (nk > 0) {
-            tmem_ld_16x256b_x4(tb + uint32_t(j0), r[0]);
-            tmem_ld_16x256b_x4(tb + (16u << 16) + uint32_t(j0), r[1]);
+#pragma unroll
+            for (int c = 0; c < Tr::kRound; ++c) {
+              tmem_ld_16x256b_x4(tb + uint32_t(j0 + 32 * c), r[2 * c]);
+              tmem_ld_16x256b_x4(tb + (16u << 16) + uint32_t(j0 + 32 * c), r[2 * c + 1]);
+            }
             tmem_ld_wait_regs(r);
           } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) r[0][j] = r[1][j] = 0u;
+            for (int c = 0; c < 2 * Tr::kRound; ++c)
+#pragma unroll
+              for (int j = 0; j < 16; ++j) r[c][j] = 0u;
           }
-          stage_chunk_16(p, r, st);
+#pragma unroll
+          for (int c = 0; c < Tr::kRound; ++c)
+            stage_chunk_16(p, r[2 * c], r[2 * c + 1], st + c * Tr::kChunk);
           if (!bulk) {
             __syncwarp();
-            store_chunk_16(p, st, static_cast<uint16_t*>(p.out) + base + j0 * p.ldo, cw,
-                           nr - j0);
+#pragma unroll
+            for (int c = 0; c < Tr::kRound; ++c)
+              store_chunk_16(p, st + c * Tr::kChunk,
+                             static_cast<uint16_t*>(p.out) + base + (j0 + 32 * c) * p.ldo, cw,
+                             nr - j0 - 32 * c);
             __syncwarp();
           }
         }
@@ -681,7 +697,8 @@ moe_status run_variant(GroupedArgs& a, const Operand& A, const Operand& B, int d
                            : a.fmt  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                            EB, a.out, uint64_t(a.C), uint64_t(a.R), uint64_t(a.groups),
-                           uint64_t(a.ldo) * EB, uint64_t(a.group_stride) * EB, 32, 32 * EB);
+                           uint64_t(a.ldo) * EB, uint64_t(a.group_stride) * EB, 32 * V::Tr::kRound,
+                           32 * EB);
   if (!ok) return MOE_ERR_CUDA;
   if (V::launch(a, dev, sms, V::tiles_of(a), stream) != cudaSuccess) {
     cudaGetLastError();
@@ -720,7 +737,7 @@ moe_status dispatch(GroupedArgs& a, const Operand& A, const Operand& B, bool out
     return run_variant<M, 2, 256, 2, 3, 2>(a, A, B, dev, sms, stream);
   } else {
     if (out_f32) return run_variant<M, 2, 256, 1, 5, 4>(a, A, B, dev, sms, stream);
-    return run_variant<M, 2, 256, 1, 6, 2>(a, A, B, dev, sms, stream);
+    return run_variant<M, 2, 256, 1, 5, 2>(a, A, B, dev, sms, stream);
   }
 }
 
