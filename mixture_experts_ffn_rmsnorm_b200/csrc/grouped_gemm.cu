@@ -24,7 +24,7 @@
 // shared between calls).
 //   warp 0    one lane issues the TMA loads into a ring of stages;
 //   warp 1    one lane (of the pair's rank 0) issues tcgen05.mma;
-//   warp 2    weight gradient: zeroes the rows of a group's last k-block that
+//   warps 2, 3 weight gradient: zero the rows of a group's last k-block that
 //             belong to the next group, in shared memory;
 //   warps 4-11 read the accumulators from TMEM and store them, while the MMA
 //             warp fills the other accumulator.
@@ -279,13 +279,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* staging = tiles + STAGES * Tr::kStageBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + Tr::kStagingBytes);
   uint64_t* empty = full + STAGES;
-  uint64_t* tail = empty + STAGES;
-  uint64_t* tfull = tail + STAGES;
+  uint64_t* tail = empty + STAGES;  // two sets, one for each of the warps 2 and 3
+  uint64_t* tfull = tail + 2 * STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((3 * STAGES + 5) * 8 + 8 <= 512, "");
+  static_assert((4 * STAGES + 5) * 8 + 8 <= 512, "");
   __shared__ int s_pre[MOE_MAX_EXPERTS + 1];
   __shared__ int s_scan[kThreads / 32];
   __shared__ int s_rows[2 * MOE_MAX_EXPERTS];  // {first row, rows} of each group
@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[s], CG);
       mbar_init(&empty[s], 1);
       mbar_init(&tail[s], 1);
+      mbar_init(&tail[STAGES + s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    int stage = 0;
+    int stage = 0, tails = 0;
     uint32_t phase = 0;
     bool ok = true;
     while (ok && uniform(walk.next(p, s_rows, s_pre))) {
@@ -376,13 +377,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const int kbn = min(KPS, nk - kb0);
         const uint32_t bytes = uint32_t(kbn) * (Tr::kABytes + bbytes);
-        const bool is_tail = M == kWgrad && kb0 + 1 == nk && (cnt & (kBK - 1)) != 0;
+        const bool is_tail = M == kWgrad && kb0 + 1 == nk && (cnt & 15) != 0;
         const uint32_t st = tiles_u32 + stage * Tr::kStageBytes;
         if (elect_one()) {
           uint32_t bar;
           if (is_tail) {
-            mbar_arrive_expect_tx(&tail[stage], bytes);
-            bar = smem_u32(&tail[stage]);
+            uint64_t* tb = &tail[(tails & 1) * STAGES + stage];
+            mbar_arrive_expect_tx(tb, bytes);
+            bar = smem_u32(tb);
           } else if (CG == 2) {
             bar = map_to_rank(smem_u32(&full[stage]), 0);
             mbar_arrive_expect_tx_at(bar, bytes);
@@ -412,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
+        tails += is_tail;
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;
@@ -447,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int last = (cnt - (nk - 1) * kBK + 15) / 16;  // weight gradient: steps with rows
         for (int kb0 = 0; kb0 < nk; kb0 += KPS) {
           // a group's last k-block: the pair's warps 2 may have written to it
-          const bool is_tail = M == kWgrad && kb0 + 1 == nk && (cnt & (kBK - 1)) != 0;
+          const bool is_tail = M == kWgrad && kb0 + 1 == nk && (cnt & 15) != 0;
           ok = uniform(CG == 2 && is_tail ? mbar_wait_acquire_cluster(&full[stage], phase, abort)
                                           : mbar_wait(&full[stage], phase, abort));
           if (!ok) break;
@@ -488,24 +491,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       int zero = 0;
       mbar_wait(drain, 0, &zero);
     }
-  } else if (M == kWgrad && warp == 2) {
+  } else if (M == kWgrad && (warp == 2 || warp == 3)) {
     // ---------------------------------------- rows behind a group's last one
-    int total = 0;
-    uint32_t used = 0;  // phase bit of each stage's tail barrier
+    // Two warps take turns: clearing, the fences and the hand-over to the
+    // pair's other CTA take about a microsecond, a tile of one k-block 0.5.
+    // Each has barriers of its own: neighbouring tails may share a stage, and
+    // a barrier that completes a phase for the other warp in between would
+    // answer this one's wait too early.
+    int total = 0, tails = 0;
+    uint32_t used = 0;  // phase bit of each of this warp's barriers
+    uint64_t* mine = tail + (warp - 2) * STAGES;
     while (walk.next(p, s_rows, s_pre)) {
       const GTile& t = walk.t;
       total += t.nk;
-      const int valid = t.cnt & (kBK - 1);
-      if (valid == 0) continue;
+      if ((t.cnt & 15) == 0) continue;  // whole steps of 16 rows
+      if ((tails++ & 1) != warp - 2) continue;
       const int stage = (total - 1) % STAGES;
-      if (!mbar_wait(&tail[stage], (used >> stage) & 1u, abort)) {
+      if (!mbar_wait(&mine[stage], (used >> stage) & 1u, abort)) {
         give_up(p, abort);
         break;
       }
       used ^= 1u << stage;
       const int nb = ((t.nr + 15) & ~15) / CG;
       const int blocks = 2 + (nb + 63) / 64;
-      const int end = (valid + 15) & ~15;
+      const int valid = t.cnt & (kBK - 1), end = (valid + 15) & ~15;
       for (int h = 0; h < blocks; ++h) {
         uint32_t* blk = reinterpret_cast<uint32_t*>(tiles + stage * Tr::kStageBytes + h * 8192);
         for (int r = valid; r < end; ++r) blk[r * 32 + lane] = 0u;  // whole rows: swizzled or not
@@ -513,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        if (CG == 2)
+        if (CG == 2 && rank != 0)
           mbar_arrive_release_at(map_to_rank(smem_u32(&full[stage]), 0));
         else
           mbar_arrive(&full[stage]);

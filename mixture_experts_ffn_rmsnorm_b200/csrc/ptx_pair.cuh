@@ -70,8 +70,17 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_at(uint32_t cluster_addr, 
 __device__ __forceinline__ bool mbar_wait_acquire_cluster(uint64_t* bar, uint32_t parity,
                                                           volatile int* abort) {
   if (!mbar_wait(bar, parity, abort)) return false;
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
-  return true;
+  // the phase is complete: this returns at once (a fence.acq_rel.cluster in
+  // its place took 0.4 us)
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // 3-D tiled load of one box into this CTA's shared memory.  CG = 2: the
@@ -92,15 +101,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
-}
-
-// Bring one box into L2 (no shared memory, no completion).
-__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int32_t x, int32_t y,
-                                                int32_t z) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(z)
-               : "memory");
 }
 
 // 3-D tiled store of one box from shared memory, in this thread's current

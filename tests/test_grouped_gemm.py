@@ -180,6 +180,13 @@ def test_weight_gradient_in_32_bits_and_accumulated(counts):
     assert torch.equal(dw[1], before[1])  # nothing to add to an empty group
 
 
+@pytest.mark.parametrize("f32", (False, True))
+@pytest.mark.parametrize("blocks", (1, 2, 4, 5, 6))
+def test_tails_of_neighbouring_tiles_in_one_stage(blocks, f32):
+    # every group ends inside the same k-block of the ring, tile after tile on each CTA pair
+    run("wgrad", [64 * blocks - 3] * 24, K=768, N=1536, dtype="bf16", f32=f32, seed=blocks)
+
+
 @pytest.mark.parametrize("bad", (float("inf"), float("nan")))
 @pytest.mark.parametrize("counts", ([10, 7, 3, 50], [400, 13, 77, 110]), ids=("few", "many"))
 def test_nonfinite_values_stay_in_their_group(counts, bad):
