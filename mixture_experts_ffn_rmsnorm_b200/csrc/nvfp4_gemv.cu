@@ -27,9 +27,9 @@
 // pass as one tile of 128 rows (the MMA's M) where it can.
 //   warp 16    TMA: 256 inputs (128 bytes) of a tile's rows into a ring stage,
 //              and the tile's scales as one copy;
-//   warps 0-3  the MMAs, every fourth stage of a tile each and into an
-//              accumulator of its own: a thread takes 1300 cycles to wait for a
-//              stage and issue its four MMAs, the MMAs themselves about 600;
+//   warps 0-3  the MMAs, every third or fourth stage each and into an
+//              accumulator of its own: a warp takes longer to wait for a stage
+//              and issue its four MMAs than the MMAs themselves take;
 //   warps 4-7  epilogue: a lane is a weight row, so the lanes' results are
 //              neighbours in y;
 //   warps 12-15 scales from shared memory through registers into TMEM, a
@@ -58,7 +58,7 @@ constexpr int kMaxRows = MOE_NVFP4_MAX_ROWS;
 constexpr int kGemvSmemMax = 232448;
 // TMEM columns: two accumulators (of kChains each), the tokens' scales (ones),
 // the stages' scales (16 columns each: 4 bytes of a row per 64 inputs, 4 x 32 rows)
-constexpr int kChains = 4;  // MMA warps
+constexpr int kChains = 4;  // MMA warps, at most
 constexpr uint32_t kAccCols = kMaxPassRows * kDigits;
 constexpr uint32_t kColSfb = 2 * kChains * kAccCols;
 constexpr uint32_t kColSfa = kColSfb + 16;
@@ -85,6 +85,7 @@ struct GemvArgs {
   int rp;      // rows of a pass, at most (1, 2 or 4)
   int xrows;   // digit rows kept in shared memory: max(rp * 8, 16)
   int stages;
+  int issuers;    // MMA warps (3 or 4); divides stages
   int raws;       // tiles whose scales are in shared memory (1 or 2)
   int raw_bytes;  // of one tile
 };
@@ -376,7 +377,8 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
   const int xblock = p.xrows * 128;               // digit rows of one stage's inputs
   uint8_t* raw = xs + nst * xblock;               // tiles' scales as they are stored
   const int row_bytes = p.K / 16;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring_u32 = smem_u32(ring), xs_u32 = smem_u32(xs);
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
   if (tid == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -385,7 +387,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&tfull[b], kChains);
+      mbar_init(&tfull[b], p.issuers);
       mbar_init(&tempty[b], 4);
       mbar_init(&raw_full[b], 1);
       mbar_init(&raw_empty[b], 4);
@@ -483,7 +485,11 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     }
   } else if (warp < kChains) {
     // --------------------------------------------------------- MMA issuers
-    if (lane == 0) {
+    // Warp w takes the stages whose number in the CTA's sequence is w modulo
+    // `issuers`, which divides the ring: a ring stage has one issuer for good,
+    // so no wait can be answered by a phase that another issuer left open.
+    // The warp walks with warp-uniform values, one lane issues.
+    if (warp < p.issuers) {
       int base = 0, it = 0, seen = -1;  // stages before the tile, tiles, pass
       uint32_t xphase = 0;
       bool ok = true;
@@ -491,40 +497,45 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
         const int pass = u / blocks, block = u - pass * blocks;
         two = u + 1 < u1 && block + 1 < blocks ? 2 : 1;
         if (pass != seen) {
-          if (!wait_for(p, &xfull, xphase, &S.abort)) break;
+          if (!uniform(wait_for(p, &xfull, xphase, &S.abort))) break;
           xphase ^= 1u;
           seen = pass;
         }
-        const int cols = max(16, (S.pass_n[pass] * kDigits + 15) & ~15);
+        const int cols = max(16, (uniform(int(S.pass_n[pass])) * kDigits + 15) & ~15);
         const uint32_t idesc = nvfp4_idesc(cols);
         const uint32_t d = tmem + uint32_t((it & 1) * kChains + warp) * kAccCols;
-        if (!wait_for(p, &tempty[it & 1], ((it >> 1) & 1) ^ 1u, &S.abort)) break;
+        if (!uniform(wait_for(p, &tempty[it & 1], ((it >> 1) & 1) ^ 1u, &S.abort))) break;
         tc_fence_after();
-        for (int k = warp; k < nst; k += kChains) {
+        const int rot = base % p.issuers;
+        const int k0 = warp >= rot ? warp - rot : warp - rot + p.issuers;
+        for (int k = k0; k < nst; k += p.issuers) {
           const int stage = (base + k) % p.stages;
           const uint32_t phase = ((base + k) / p.stages) & 1;
-          if (!wait_for(p, &full[stage], phase, &S.abort) ||
-              !wait_for(p, &sf_full[stage], phase, &S.abort)) {
-            ok = false;
-            break;
-          }
+          ok = uniform(wait_for(p, &full[stage], phase, &S.abort) &&
+                       wait_for(p, &sf_full[stage], phase, &S.abort));
+          if (!ok) break;
           tc_fence_after();
           const uint32_t sfa = tmem + kColSfa + stage * 16;
           const int steps = min(4, (p.K - k * kStageK + 63) / 64);
-          const uint64_t ad = smem_desc_sw128(ring + stage * kStageBytes);
-          const uint64_t bd = smem_desc_sw128(xs + k * xblock);
+          const uint64_t ad = smem_desc_k_sw128(ring_u32 + stage * kStageBytes);
+          const uint64_t bd = smem_desc_k_sw128(xs_u32 + k * xblock);
+          if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j < steps)
-              umma_nvfp4(d, ad + j * 2, bd + j * 2, idesc, sfa + j * 4, tmem + kColSfb,
-                         k >= kChains || j > 0);
-          umma_commit(&empty[stage]);
+            for (int j = 0; j < 4; ++j)
+              if (j < steps)
+                umma_nvfp4(d, ad + j * 2, bd + j * 2, idesc, sfa + j * 4, tmem + kColSfb,
+                           k > k0 || j > 0);
+            umma_commit(&empty[stage]);
+          }
+          __syncwarp();
         }
-        if (ok) umma_commit(&tfull[it & 1]);
+        if (ok && elect_one()) umma_commit(&tfull[it & 1]);
+        __syncwarp();
         base += nst;
         ++it;
       }
-      umma_commit(&drain[warp]);
+      if (elect_one()) umma_commit(&drain[warp]);
+      __syncwarp();
       int zero = 0;
       mbar_wait(&drain[warp], 0, &zero);
     }
@@ -621,7 +632,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
       if (warp < 8) {
         // ---------------------------------------------------------- epilogue
         const float s2 = p.scale2[e];
-        const int chains = min(kChains, nst);  // accumulators in use
+        const int chains = min(p.issuers, nst);  // accumulators in use
         for (int u = ub, two; u < ue; u += two) {
           two = u + 1 < ue ? 2 : 1;
           const int n0 = (u - pass * blocks) * kUnitRows;
@@ -632,10 +643,13 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
           const uint32_t d = tmem + (uint32_t(cw * 32) << 16) +
                              uint32_t(it & 1) * kChains * kAccCols;
           for (int n = 0; n < n_rows && cw * 32 < valid; ++n) {
+            // chain c: the stages c, c + issuers, ... of the tile
             uint32_t acc[kChains][kDigits];
 #pragma unroll
-            for (int c = 0; c < kChains; ++c)
-              tmem_ld_32x32b_n<kDigits>(d + c * kAccCols + uint32_t(n * kDigits), acc[c]);
+            for (int c = 0; c < kChains; ++c) {
+              const uint32_t w = c < chains ? uint32_t(it * nst + c) % p.issuers : 0;
+              tmem_ld_32x32b_n<kDigits>(d + w * kAccCols + uint32_t(n * kDigits), acc[c]);
+            }
             tmem_ld_wait_regs(acc);
             float v = 0.f;
 #pragma unroll
@@ -836,6 +850,8 @@ extern "C" moe_status moe_nvfp4_gemv(const void* x, int64_t ldx, int32_t x_per_s
       break;
   }
   if (a.stages > kMaxStages) a.stages = kMaxStages;
+  a.issuers = a.stages / 3 * 3 > a.stages / 4 * 4 ? 3 : 4;
+  a.stages = a.stages / a.issuers * a.issuers;
   const long long most = (long long)(a.R) * ((N + kUnitRows - 1) / kUnitRows);
   const int grid = int(most < sms ? most : sms);
   const int smem = 1024 + a.stages * kStageBytes + nst * a.xrows * 128 + a.raws * a.raw_bytes;
