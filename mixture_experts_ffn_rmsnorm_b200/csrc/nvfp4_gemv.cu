@@ -435,52 +435,51 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
   // two units where this CTA has both of a pass.
   if (warp == kProducer) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int stage = 0, it = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int u = u0, two; u < u1 && ok; u += two) {
-        const int pass = u / blocks, block = u - pass * blocks;
-        two = u + 1 < u1 && block + 1 < blocks ? 2 : 1;
-        const int row = S.pass_e[pass] * p.N + block * kUnitRows;
-        {
-          // the rows' scales: the 16-byte blocks that hold them, and the
-          // tensor's last bytes, fewer than 16, by plain loads
-          const int slot = it % p.raws;
-          if (!wait_for(p, &raw_empty[slot], ((it / p.raws) & 1) ^ 1u, &S.abort)) {
-            ok = false;
-            break;
-          }
-          const long long a = (long long)(row)*row_bytes;
-          const long long end = a + min(two * kUnitRows, p.N - block * kUnitRows) * row_bytes;
-          const long long a16 = a & ~15LL, whole = p.scale_bytes & ~15LL;
-          const long long b16 = min((end + 15) & ~15LL, whole);
-          uint8_t* dst = raw + slot * p.raw_bytes;
+    int stage = 0, it = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = u0, two; u < u1 && ok; u += two, ++it) {
+      const int pass = u / blocks, block = u - pass * blocks;
+      two = u + 1 < u1 && block + 1 < blocks ? 2 : 1;
+      const int row = uniform(int(S.pass_e[pass])) * p.N + block * kUnitRows;
+      const int slot = it % p.raws;
+      ok = uniform(wait_for(p, &raw_empty[slot], ((it / p.raws) & 1) ^ 1u, &S.abort));
+      if (!ok) break;
+      {
+        // the rows' scales: the 16-byte blocks that hold them, and the
+        // tensor's last bytes, fewer than 16, by plain loads
+        const long long a = (long long)(row)*row_bytes;
+        const long long end = a + min(two * kUnitRows, p.N - block * kUnitRows) * row_bytes;
+        const long long a16 = a & ~15LL, whole = p.scale_bytes & ~15LL;
+        const long long b16 = min((end + 15) & ~15LL, whole);
+        uint8_t* dst = raw + slot * p.raw_bytes;
+        if (elect_one()) {
           for (long long i = b16; i < end; ++i) dst[i - a16] = p.scale[i];
           mbar_arrive_expect_tx(&raw_full[slot], uint32_t(b16 - a16));
           if (b16 > a16)
             bulk_load(smem_u32(dst), p.scale + a16, uint32_t(b16 - a16), &raw_full[slot]);
-          ++it;
         }
-        for (int k = 0; k < nst; ++k) {
-          if (!wait_for(p, &empty[stage], phase ^ 1u, &S.abort)) {
-            ok = false;
-            break;
-          }
+        __syncwarp();
+      }
+      for (int k = 0; k < nst; ++k) {
+        ok = uniform(wait_for(p, &empty[stage], phase ^ 1u, &S.abort));
+        if (!ok) break;
+        if (elect_one()) {
+          const uint32_t bar = smem_u32(&full[stage]), st = ring_u32 + stage * kStageBytes;
           mbar_arrive_expect_tx(&full[stage], two * 8192);
-          for (int h = 0; h < two; ++h)
-            tma_load_3d<1>(smem_u32(ring + stage * kStageBytes + h * 8192), &p.tmW,
-                           smem_u32(&full[stage]), k * 128, row + h * kUnitRows, 0);
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          tma_load_3d<1>(st, &p.tmW, bar, k * 128, row, 0);
+          if (two == 2) tma_load_3d<1>(st + 8192, &p.tmW, bar, k * 128, row + kUnitRows, 0);
+        }
+        __syncwarp();
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok) {
-        const long long t0 = clock64();  // let the copies in flight land
-        while (clock64() - t0 < 4000000) {
-        }
+    }
+    if (!ok) {
+      const long long t0 = clock64();  // let the copies in flight land
+      while (clock64() - t0 < 4000000) {
       }
     }
   } else if (warp < kChains) {
