@@ -25,18 +25,18 @@
 // matrix.  All passes' blocks of 64 weight rows ("units") form one list, cut
 // into contiguous ranges, one per CTA; a CTA takes two neighbouring units of a
 // pass as one tile of 128 rows (the MMA's M) where it can.
-//   warp 16    TMA: 256 inputs (128 bytes) of a tile's rows into a ring stage,
+//   warp 20    TMA: 256 inputs (128 bytes) of a tile's rows into a ring stage,
 //              and the tile's scales as one copy;
 //   warps 0-3  the MMAs, every third or fourth stage each and into an
 //              accumulator of its own: a warp takes longer to wait for a stage
 //              and issue its four MMAs than the MMAs themselves take;
 //   warps 4-7  epilogue: a lane is a weight row, so the lanes' results are
 //              neighbours in y;
-//   warps 12-15 scales from shared memory through registers into TMEM, a
+//   warps 8-11 scales from shared memory through registers into TMEM, a
 //              lane quarter each (read from global memory by the row, 4 to 8
 //              bytes a lane, they took 1000 cycles a stage; handed on with
 //              tcgen05.cp, the four copies of a stage held up its MMAs);
-//   warps 4-11 the token rows' digits, at the start of each pass.
+//   warps 12-19 the token rows' digits, a pass ahead of its MMAs.
 // Results do not depend on the grid.
 #include <cuda_fp16.h>
 
@@ -46,8 +46,8 @@
 namespace moe {
 namespace {
 
-constexpr int kGemvThreads = 544;
-constexpr int kProducer = 16;  // warp
+constexpr int kGemvThreads = 672;
+constexpr int kProducer = 20;  // warp
 constexpr int kUnitRows = 64;
 constexpr int kDigits = 8;
 constexpr int kMaxPassRows = 4;
@@ -64,7 +64,7 @@ constexpr uint32_t kColSfb = 2 * kChains * kAccCols;
 constexpr uint32_t kColSfa = kColSfb + 16;
 constexpr uint32_t kTmemCols = 512;
 static_assert(kColSfa + kMaxStages * 16 <= kTmemCols, "");
-constexpr int kConverters = 8 * 32;  // threads that write digits (warps 4-11)
+constexpr int kConverters = 8 * 32;  // threads that write digits
 
 struct GemvArgs {
   CUtensorMap tmW;  // [E * N, K / 2] bytes, boxes of 128 bytes x 64 rows
@@ -86,6 +86,7 @@ struct GemvArgs {
   int xrows;   // digit rows kept in shared memory: max(rp * 8, 16)
   int stages;
   int issuers;    // MMA warps (3 or 4); divides stages
+  int xbufs;      // passes whose digits are in shared memory (1 or 2)
   int raws;       // tiles whose scales are in shared memory (1 or 2)
   int raw_bytes;  // of one tile
 };
@@ -100,12 +101,12 @@ struct Setup {
   int count[MOE_MAX_EXPERTS];
   int first[MOE_MAX_EXPERTS];
   int passes;
-  int xrow[kMaxPassRows];    // token rows staged (-1: none)
-  int shift[kMaxPassRows];   // s of each staged row
-  int odd[kMaxPassRows];     // the row holds an infinity or a NaN
+  int xrow[2][kMaxPassRows];   // token rows in each digit buffer
+  int shift[2][kMaxPassRows];  // their s
+  int odd[2][kMaxPassRows];    // the row holds an infinity or a NaN
   float amax[kMaxPassRows][8];
   int bad[kMaxPassRows][8];
-  int changed;  // the last pass whose token rows differ from the staged ones
+  int changed;  // the last pass whose token rows differ from those of its buffer
   volatile int abort;
 };
 
@@ -368,14 +369,15 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ Setup S;
   __shared__ uint64_t full[kMaxStages], sf_full[kMaxStages], empty[kMaxStages];
-  __shared__ uint64_t tfull[2], tempty[2], raw_full[2], raw_empty[2], xfull, drain[kChains];
+  __shared__ uint64_t tfull[2], tempty[2], raw_full[2], raw_empty[2], xfull[2], xempty[2];
+  __shared__ uint64_t drain[kChains];
   __shared__ uint32_t tmem_slot;
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* ring = smem_raw + pad;                 // the stages
   uint8_t* xs = ring + p.stages * kStageBytes;    // the digits
   const int nst = (p.K + kStageK - 1) / kStageK;  // stages of a tile
   const int xblock = p.xrows * 128;               // digit rows of one stage's inputs
-  uint8_t* raw = xs + nst * xblock;               // tiles' scales as they are stored
+  uint8_t* raw = xs + p.xbufs * nst * xblock;           // tiles' scales as they are stored
   const int row_bytes = p.K / 16;
   const uint32_t ring_u32 = smem_u32(ring), xs_u32 = smem_u32(xs);
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -389,10 +391,11 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], p.issuers);
       mbar_init(&tempty[b], 4);
+      mbar_init(&xfull[b], 1);
+      mbar_init(&xempty[b], 4);
       mbar_init(&raw_full[b], 1);
       mbar_init(&raw_empty[b], 4);
     }
-    mbar_init(&xfull, 1);
     for (int c = 0; c < kChains; ++c) mbar_init(&drain[c], 1);
     fence_barrier_init();
     tma_prefetch_desc(&p.tmW);
@@ -402,7 +405,8 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     tmem_alloc(&tmem_slot, kTmemCols);
     tmem_relinquish();
   }
-  if (tid < kMaxPassRows) S.xrow[tid] = -2;
+  if (tid < 2 * kMaxPassRows) S.xrow[tid / kMaxPassRows][tid % kMaxPassRows] = -2;
+  if (tid == 0) S.changed = -1;
   pdl_wait();
   pdl_trigger();
   // ---- passes: routed rows grouped by expert, at most rp rows each
@@ -489,27 +493,27 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     // so no wait can be answered by a phase that another issuer left open.
     // The warp walks with warp-uniform values, one lane issues.
     if (warp < p.issuers) {
-      int base = 0, it = 0, seen = -1;  // stages before the tile, tiles, pass
-      uint32_t xphase = 0;
+      int it = 0, seen = -1, passes = -1;  // tiles; the pass, and how many before it
+      int stage = warp, k0 = warp;        // this warp's next stage, and its first of the tile
+      uint32_t phase = 0;
       bool ok = true;
       for (int u = u0, two; u < u1 && ok; u += two) {
         const int pass = u / blocks, block = u - pass * blocks;
         two = u + 1 < u1 && block + 1 < blocks ? 2 : 1;
         if (pass != seen) {
-          if (!uniform(wait_for(p, &xfull, xphase, &S.abort))) break;
-          xphase ^= 1u;
           seen = pass;
+          ++passes;
+          if (!uniform(wait_for(p, &xfull[passes % p.xbufs], (passes / p.xbufs) & 1, &S.abort)))
+            break;
         }
         const int cols = max(16, (uniform(int(S.pass_n[pass])) * kDigits + 15) & ~15);
         const uint32_t idesc = nvfp4_idesc(cols);
         const uint32_t d = tmem + uint32_t((it & 1) * kChains + warp) * kAccCols;
+        const uint32_t xb = xs_u32 + passes % p.xbufs * nst * xblock;
         if (!uniform(wait_for(p, &tempty[it & 1], ((it >> 1) & 1) ^ 1u, &S.abort))) break;
         tc_fence_after();
-        const int rot = base % p.issuers;
-        const int k0 = warp >= rot ? warp - rot : warp - rot + p.issuers;
-        for (int k = k0; k < nst; k += p.issuers) {
-          const int stage = (base + k) % p.stages;
-          const uint32_t phase = ((base + k) / p.stages) & 1;
+        int k = k0;
+        for (; k < nst; k += p.issuers) {
           ok = uniform(wait_for(p, &full[stage], phase, &S.abort) &&
                        wait_for(p, &sf_full[stage], phase, &S.abort));
           if (!ok) break;
@@ -517,7 +521,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
           const uint32_t sfa = tmem + kColSfa + stage * 16;
           const int steps = min(4, (p.K - k * kStageK + 63) / 64);
           const uint64_t ad = smem_desc_k_sw128(ring_u32 + stage * kStageBytes);
-          const uint64_t bd = smem_desc_k_sw128(xs_u32 + k * xblock);
+          const uint64_t bd = smem_desc_k_sw128(xb + k * xblock);
           if (elect_one()) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -527,10 +531,15 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
             umma_commit(&empty[stage]);
           }
           __syncwarp();
+          stage += p.issuers;
+          if (stage >= p.stages) {
+            stage -= p.stages;
+            phase ^= 1u;
+          }
         }
+        k0 = k - nst;
         if (ok && elect_one()) umma_commit(&tfull[it & 1]);
         __syncwarp();
-        base += nst;
         ++it;
       }
       if (elect_one()) umma_commit(&drain[warp]);
@@ -538,152 +547,160 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
       int zero = 0;
       mbar_wait(&drain[warp], 0, &zero);
     }
-  } else if (warp < 12) {
-    // ----------------------------------------------- digits, then epilogue
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ epilogue
     const int cw = warp - 4;
-    int it = 0;
-    for (int ub = u0; ub < u1;) {
-      const int pass = ub / blocks;
+    int it = 0, passes = 0;
+    for (int ub = u0; ub < u1; ++passes) {
+      const int pass = ub / blocks, b = passes % p.xbufs;
       const int ue = min(u1, (pass + 1) * blocks);  // this CTA's units of the pass
       const int n_rows = S.pass_n[pass], e = S.pass_e[pass];
       const int16_t* rows = S.sorted + S.pass_at[pass];
-      {
-        // a row's 256-wide blocks over 8, 4, 2 or 1 warps
-        const int per = n_rows > 4 ? 1 : n_rows > 2 ? 2 : n_rows > 1 ? 4 : 8;
-        const int n = cw / per, part = cw % per;
-        const int want = n < n_rows ? (p.per_slot ? rows[n] : rows[n] / p.top_k) : -1;
-        // the pass before is done: its epilogues are, so its MMAs are
-        named_barrier(1, kConverters);
-        if (lane == 0 && part == 0 && want >= 0 && S.xrow[n] != want) S.changed = pass;
-        named_barrier(1, kConverters);
-        if (S.changed == pass) {
-          const uint16_t* xr = static_cast<const uint16_t*>(p.x) + (want < 0 ? 0 : want) * p.ldx;
-          // a lane's first two chunks of 8 elements stay in registers
-          const int k0 = part * 256 + lane * 8, kstep = per * 256;
-          uint4 held[2];
-          if (want >= 0) {
-            float m = 0.f;
-            int bad = 0;
+      const float s2 = p.scale2[e];
+      const int chains = min(p.issuers, nst);  // accumulators in use
+      wait_for(p, &xfull[b], (passes / p.xbufs) & 1, &S.abort);  // the rows' s
+      for (int u = ub, two; u < ue; u += two) {
+        two = u + 1 < ue ? 2 : 1;
+        const int n0 = (u - pass * blocks) * kUnitRows;
+        const int valid = min(two * kUnitRows, p.N - n0);  // weight rows of the tile
+        const int r = cw * 32 + lane;
+        const bool ok = wait_for(p, &tfull[it & 1], (it >> 1) & 1, &S.abort);
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t(cw * 32) << 16) +
+                           uint32_t(it & 1) * kChains * kAccCols;
+        for (int n = 0; n < n_rows && cw * 32 < valid; ++n) {
+          // chain c: the stages c, c + issuers, ... of the tile
+          uint32_t acc[kChains][kDigits];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              held[i] = k0 + i * kstep < p.K
-                            ? *reinterpret_cast<const uint4*>(xr + k0 + i * kstep)
-                            : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) amax8<BF16>(held[i], m, bad);
-            for (int k = k0 + 2 * kstep; k < p.K; k += kstep)
-              amax8<BF16>(*reinterpret_cast<const uint4*>(xr + k), m, bad);
-#pragma unroll
-            for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-            bad = __any_sync(0xffffffffu, bad);
-            if (lane == 0) {
-              S.amax[n][part] = m;
-              S.bad[n][part] = bad;
-            }
+          for (int c = 0; c < kChains; ++c) {
+            const uint32_t w = c < chains ? uint32_t(it * nst + c) % p.issuers : 0;
+            tmem_ld_32x32b_n<kDigits>(d + w * kAccCols + uint32_t(n * kDigits), acc[c]);
           }
-          named_barrier(1, kConverters);
-          if (want >= 0) {
-            float m = 0.f;
-            int bad = 0;
-            for (int i = 0; i < per; ++i) {
-              m = fmaxf(m, S.amax[n][i]);
-              bad |= S.bad[n][i];
-            }
-            // the largest magnitude to [2^21, 2^22); a float32's exponent, or a subnormal's
-            const uint32_t mb = __float_as_uint(m);
-            const int ex = mb >> 23 ? int(mb >> 23) - 127 : -118 - __clz(mb | 1u);
-            const int sh = mb ? 21 - ex : 0;
-            const float f1 = pow2(sh / 2), f2 = pow2(sh - sh / 2);
-            if (lane == 0 && part == 0) {
-              S.xrow[n] = want;
-              S.shift[n] = sh;
-              S.odd[n] = bad;
-            }
-            auto put = [&](int k, const uint4& u) {
-              uint32_t w[8];
-              float v[8];
-              to_float8<BF16>(u, v);
+          tmem_ld_wait_regs(acc);
+          float v = 0.f;
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                w[i] = digit_codes(finite(v[i]) ? __float2int_rn(v[i] * f1 * f2) : 0);
-              transpose_nibbles(w);
-              // digit i of eight inputs: 4 bytes of row n * 8 + i, swizzled as TMA would
-              uint8_t* dst = xs + (k / kStageK) * xblock + n * kDigits * 128 + (lane & 3) * 4;
+          for (int i = kDigits - 1; i >= 0; --i) {
+            float t = __uint_as_float(acc[0][i]);
 #pragma unroll
-              for (int i = 0; i < kDigits; ++i)
-                *reinterpret_cast<uint32_t*>(dst + i * 128 + ((lane >> 2) ^ i) * 16) = w[i];
-            };
-            // zeros behind K, to the end of the last stage
-            // (one copy of the code: it runs cold)
-#pragma unroll 1
-            for (int k = k0, i = 0; k < nst * kStageK; k += kstep, ++i) {
-              uint4 u = i == 0 ? held[0] : held[1];
-              if (i > 1)
-                u = k < p.K ? *reinterpret_cast<const uint4*>(xr + k) : make_uint4(0, 0, 0, 0);
-              put(k, u);
-            }
+            for (int c = 1; c < kChains; ++c)
+              if (c < chains) t += __uint_as_float(acc[c][i]);
+            v = fmaf(v, 8.f, t);
           }
-          fence_proxy_async_smem();
-          named_barrier(1, kConverters);
-        }
-        if (warp == 4 && lane == 0) mbar_arrive(&xfull);
-      }
-      if (warp < 8) {
-        // ---------------------------------------------------------- epilogue
-        const float s2 = p.scale2[e];
-        const int chains = min(p.issuers, nst);  // accumulators in use
-        for (int u = ub, two; u < ue; u += two) {
-          two = u + 1 < ue ? 2 : 1;
-          const int n0 = (u - pass * blocks) * kUnitRows;
-          const int valid = min(two * kUnitRows, p.N - n0);  // weight rows of the tile
-          const int r = cw * 32 + lane;
-          const bool ok = wait_for(p, &tfull[it & 1], (it >> 1) & 1, &S.abort);
-          tc_fence_after();
-          const uint32_t d = tmem + (uint32_t(cw * 32) << 16) +
-                             uint32_t(it & 1) * kChains * kAccCols;
-          for (int n = 0; n < n_rows && cw * 32 < valid; ++n) {
-            // chain c: the stages c, c + issuers, ... of the tile
-            uint32_t acc[kChains][kDigits];
-#pragma unroll
-            for (int c = 0; c < kChains; ++c) {
-              const uint32_t w = c < chains ? uint32_t(it * nst + c) % p.issuers : 0;
-              tmem_ld_32x32b_n<kDigits>(d + w * kAccCols + uint32_t(n * kDigits), acc[c]);
-            }
-            tmem_ld_wait_regs(acc);
-            float v = 0.f;
-#pragma unroll
-            for (int i = kDigits - 1; i >= 0; --i) {
-              float t = __uint_as_float(acc[0][i]);
-#pragma unroll
-              for (int c = 1; c < kChains; ++c)
-                if (c < chains) t += __uint_as_float(acc[c][i]);
-              v = fmaf(v, 8.f, t);
-            }
-            // digits count halves: times 2^(1 - s), in whatever range the factors lie
-            const double unscale =
-                __longlong_as_double((long long)(1023 + 1 - S.shift[n]) << 52);
-            v = float(double(v) * unscale * double(s2));
-            if (r < valid && ok && !S.abort) {
-              const long long src = p.per_slot ? rows[n] : rows[n] / p.top_k;
-              if (S.odd[n])
-                v += s2 * odd_part<BF16>(p, static_cast<const uint16_t*>(p.x) + src * p.ldx,
-                                         (long long)(e)*p.N + n0 + r);
-              if (p.relu2) v = v <= 0.f ? 0.f : v * v;  // NaN stays NaN
-              const long long o = rows[n] * p.ldy + n0 + r;
-              if constexpr (BF16)
-                static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
-              else
-                static_cast<__half*>(p.y)[o] = __float2half_rn(v);
-            }
-            __syncwarp();
+          // digits count halves: times 2^(1 - s), in whatever range the factors lie
+          const double unscale =
+              __longlong_as_double((long long)(1023 + 1 - S.shift[b][n]) << 52);
+          v = float(double(v) * unscale * double(s2));
+          if (r < valid && ok && !S.abort) {
+            const long long src = p.per_slot ? rows[n] : rows[n] / p.top_k;
+            if (S.odd[b][n])
+              v += s2 * odd_part<BF16>(p, static_cast<const uint16_t*>(p.x) + src * p.ldx,
+                                       (long long)(e)*p.N + n0 + r);
+            if (p.relu2) v = v <= 0.f ? 0.f : v * v;  // NaN stays NaN
+            const long long o = rows[n] * p.ldy + n0 + r;
+            if constexpr (BF16)
+              static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
+            else
+              static_cast<__half*>(p.y)[o] = __float2half_rn(v);
           }
-          tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&tempty[it & 1]);
-          ++it;
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[it & 1]);
+        ++it;
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&xempty[b]);
       ub = ue;
+    }
+  } else if (warp >= 12) {
+    // -------------------------------------------------------------- digits
+    const int cw = warp - 12;
+    int passes = 0;
+    for (int ub = u0; ub < u1; ++passes) {
+      const int pass = ub / blocks, b = passes % p.xbufs;
+      const int n_rows = S.pass_n[pass];
+      const int16_t* rows = S.sorted + S.pass_at[pass];
+      // a row's 256-wide blocks over 8, 4 or 2 warps
+      const int per = n_rows > 2 ? 2 : n_rows > 1 ? 4 : 8;
+      const int n = cw / per, part = cw % per;
+      const int want = n < n_rows ? (p.per_slot ? rows[n] : rows[n] / p.top_k) : -1;
+      // the pass that had this buffer is done with it: its epilogues are, so its MMAs are
+      wait_for(p, &xempty[b], ((passes / p.xbufs) & 1) ^ 1u, &S.abort);
+      if (lane == 0 && part == 0 && want >= 0 && S.xrow[b][n] != want) S.changed = pass;
+      named_barrier(1, kConverters);
+      if (S.changed == pass) {
+        const uint16_t* xr = static_cast<const uint16_t*>(p.x) + (want < 0 ? 0 : want) * p.ldx;
+        // a lane's first two chunks of 8 elements stay in registers
+        const int k0 = part * 256 + lane * 8, kstep = per * 256;
+        uint4 held[2];
+        if (want >= 0) {
+          float m = 0.f;
+          int bad = 0;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            held[i] = k0 + i * kstep < p.K
+                          ? *reinterpret_cast<const uint4*>(xr + k0 + i * kstep)
+                          : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) amax8<BF16>(held[i], m, bad);
+          for (int k = k0 + 2 * kstep; k < p.K; k += kstep)
+            amax8<BF16>(*reinterpret_cast<const uint4*>(xr + k), m, bad);
+#pragma unroll
+          for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+          bad = __any_sync(0xffffffffu, bad);
+          if (lane == 0) {
+            S.amax[n][part] = m;
+            S.bad[n][part] = bad;
+          }
+        }
+        named_barrier(1, kConverters);
+        if (want >= 0) {
+          float m = 0.f;
+          int bad = 0;
+          for (int i = 0; i < per; ++i) {
+            m = fmaxf(m, S.amax[n][i]);
+            bad |= S.bad[n][i];
+          }
+          // the largest magnitude to [2^21, 2^22); a float32's exponent, or a subnormal's
+          const uint32_t mb = __float_as_uint(m);
+          const int ex = mb >> 23 ? int(mb >> 23) - 127 : -118 - __clz(mb | 1u);
+          const int sh = mb ? 21 - ex : 0;
+          const float f1 = pow2(sh / 2), f2 = pow2(sh - sh / 2);
+          if (lane == 0 && part == 0) {
+            S.xrow[b][n] = want;
+            S.shift[b][n] = sh;
+            S.odd[b][n] = bad;
+          }
+          auto put = [&](int k, const uint4& u) {
+            uint32_t w[8];
+            float v[8];
+            to_float8<BF16>(u, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              w[i] = digit_codes(finite(v[i]) ? __float2int_rn(v[i] * f1 * f2) : 0);
+            transpose_nibbles(w);
+            // digit i of eight inputs: 4 bytes of row n * 8 + i, swizzled as TMA would
+            uint8_t* dst = xs + (b * nst + k / kStageK) * xblock + n * kDigits * 128 + (lane & 3) * 4;
+#pragma unroll
+            for (int i = 0; i < kDigits; ++i)
+              *reinterpret_cast<uint32_t*>(dst + i * 128 + ((lane >> 2) ^ i) * 16) = w[i];
+          };
+          // zeros behind K, to the end of the last stage
+          // (one copy of the code: it runs cold)
+#pragma unroll 1
+          for (int k = k0, i = 0; k < nst * kStageK; k += kstep, ++i) {
+            uint4 u = i == 0 ? held[0] : held[1];
+            if (i > 1)
+              u = k < p.K ? *reinterpret_cast<const uint4*>(xr + k) : make_uint4(0, 0, 0, 0);
+            put(k, u);
+          }
+        }
+        fence_proxy_async_smem();
+        named_barrier(1, kConverters);
+      }
+      if (warp == 12 && lane == 0) mbar_arrive(&xfull[b]);
+      ub = (pass + 1) * blocks;
     }
   } else {
     // -------------------------------------------------------------- scales
@@ -833,15 +850,18 @@ extern "C" moe_status moe_nvfp4_gemv(const void* x, int64_t ldx, int32_t x_per_s
   // most 4 (their digits take shared memory from the ring and accumulator
   // columns), fewer where the digits would leave less than four stages.
   a.rp = num_tokens > 2 ? kMaxPassRows : num_tokens;
+  if (a.rp > 2 && a.R < num_experts) a.rp = 2;  // experts with more are rare
   const int nst = (K + kStageK - 1) / kStageK;
   const int room = kGemvSmemMax - kGemvStatic - 1024;
   a.raw_bytes = 128 * (K / 16) + 32;
-  a.raws = 2;
+  a.raws = a.xbufs = 2;
   for (;;) {
     a.xrows = a.rp * kDigits < 16 ? 16 : a.rp * kDigits;
-    a.stages = (room - nst * a.xrows * 128 - a.raws * a.raw_bytes) / kStageBytes;
-    if (a.stages >= 4) break;
-    if (a.raws == 2)
+    a.stages = (room - a.xbufs * nst * a.xrows * 128 - a.raws * a.raw_bytes) / kStageBytes;
+    if (a.stages >= (a.xbufs == 2 ? 6 : 4)) break;
+    if (a.xbufs == 2)
+      a.xbufs = 1;
+    else if (a.raws == 2)
       a.raws = 1;
     else if (a.rp > 2)
       a.rp /= 2;
@@ -853,7 +873,7 @@ extern "C" moe_status moe_nvfp4_gemv(const void* x, int64_t ldx, int32_t x_per_s
   a.stages = a.stages / a.issuers * a.issuers;
   const long long most = (long long)(a.R) * ((N + kUnitRows - 1) / kUnitRows);
   const int grid = int(most < sms ? most : sms);
-  const int smem = 1024 + a.stages * kStageBytes + nst * a.xrows * 128 + a.raws * a.raw_bytes;
+  const int smem = 1024 + a.stages * kStageBytes + a.xbufs * nst * a.xrows * 128 + a.raws * a.raw_bytes;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == MOE_DTYPE_BF16;
   const int row_bytes = K / 16;  // of scales: even
