@@ -739,14 +739,35 @@ moe_status dispatch(GroupedArgs& a, const Operand& A, const Operand& B, bool out
   int dev = 0, sms = 0;
   const moe_status st = current_device(&dev, &sms);
   if (st != MOE_OK) return st;
+  // Tiles a launch is likely to have: half of the groups end in a part of a
+  // row tile.
+  const auto tiles = [&](int cg, int nb) {
+    const long long ct = (a.C + 128 * cg - 1) / (128 * cg);
+    if (M == kWgrad) return a.groups * ct * ((a.R + nb - 1) / nb);
+    const int used = a.groups < a.rows ? a.groups : a.rows;
+    return ct * (a.rows / nb + (used + 1) / 2);
+  };
   if constexpr (M != kWgrad) {
-    if (a.rows <= 64LL * a.groups) return run_variant<M, 1, 64, 2, 4, 2>(a, A, B, dev, sms, stream);
-    if (a.rows <= 128LL * a.groups)
-      return run_variant<M, 2, 128, 2, 4, 2>(a, A, B, dev, sms, stream);
+    // The row tile that covers an average group, and a smaller one where the
+    // tiles would leave SMs idle.  128 groups of K = 2688, N = 1856, forward:
+    // 1 / 48 / 64 rows 188 / 203 / 205 us with 64-row tiles, 207 / 238 / 239
+    // with 256 (64 KB of weights under way a CTA, not 48); 96 / 128 rows 219 /
+    // 229 us with 128-row tiles, 345 / 311 with 64, 244 / 281 with 256; 200
+    // rows 277 us with 256, 351 with 128.
+    int nb = a.rows <= 64LL * a.groups ? 64 : a.rows <= 128LL * a.groups ? 128 : 256;
+    if (nb == 256 && tiles(2, 256) < sms / 2) nb = 128;
+    if (nb == 128 && tiles(2, 128) < sms / 2) nb = 64;
+    if (nb == 64) return run_variant<M, 1, 64, 2, 4, 2>(a, A, B, dev, sms, stream);
+    if (nb == 128) return run_variant<M, 2, 128, 2, 4, 2>(a, A, B, dev, sms, stream);
     return run_variant<M, 2, 256, 2, 3, 2>(a, A, B, dev, sms, stream);
   } else {
-    if (out_f32) return run_variant<M, 2, 256, 1, 5, 4>(a, A, B, dev, sms, stream);
-    return run_variant<M, 2, 256, 1, 5, 2>(a, A, B, dev, sms, stream);
+    // small gradients: single CTAs and 128 x 128 tiles, four times as many
+    const bool few = tiles(2, 256) < sms / 2;
+    if (out_f32)
+      return few ? run_variant<M, 1, 128, 1, 5, 4>(a, A, B, dev, sms, stream)
+                 : run_variant<M, 2, 256, 1, 5, 4>(a, A, B, dev, sms, stream);
+    return few ? run_variant<M, 1, 128, 1, 5, 2>(a, A, B, dev, sms, stream)
+               : run_variant<M, 2, 256, 1, 5, 2>(a, A, B, dev, sms, stream);
   }
 }
 

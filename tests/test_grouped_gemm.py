@@ -150,6 +150,14 @@ def test_group_counts(mode, counts):
 
 
 @pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("rows", (1, 130, 700, 5000))
+def test_one_group_with_few_and_with_many_tiles(mode, rows):
+    # one dense matrix: the same rows as few small, many small and large tiles
+    run(mode, [rows], K=384, N=320, dtype="bf16", f32=rows == 700)
+    run(mode, [rows], K=2048, N=1536, dtype="fp16")
+
+
+@pytest.mark.parametrize("mode", MODES)
 @pytest.mark.parametrize("counts", ([9, 30, 0, 5], [90, 300, 0, 5]), ids=("few", "many"))
 def test_strides_and_rows_outside_the_groups(mode, counts):
     # operands and outputs with padded rows, rows before the first and behind the last group;
