@@ -312,6 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&p.tmB[0]);
   }
   if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, Tr::kTmemCols);
+  // (programmatic dependent launch: the above overlaps the kernel before)
+  pdl_wait();
+  pdl_trigger();
 
   // the work list: row tiles of each group, prefix sums
   {
@@ -659,13 +662,15 @@ struct Variant {
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Tr::kSmem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG > 1 ? 1 : 0;
+    cfg.numAttrs = CG > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, fn, a);
   }
 
