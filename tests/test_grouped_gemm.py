@@ -149,6 +149,16 @@ def test_group_counts(mode, counts):
     run(mode, counts, K=136, N=72, dtype="fp16")
 
 
+@pytest.mark.parametrize("dtype", ("bf16", "fp16"))
+@pytest.mark.parametrize("K,N", ((1000, 1024), (2040, 1992), (1999, 2001)))
+@pytest.mark.parametrize("mode", MODES)
+def test_ragged_groups_with_many_tiles(mode, K, N, dtype):
+    # enough tiles that the CTA pairs take them, 128 or 256 rows at a time
+    run(mode, MANY, K=K, N=N, dtype=dtype, relu2=mode == "fwd", start=3, tail=2)
+    if dtype == "bf16":
+        run(mode, [700, 0, 90, 1030, 256, 257], K=K, N=N, dtype=dtype, f32=True)
+
+
 @pytest.mark.parametrize("mode", MODES)
 @pytest.mark.parametrize("rows", (1, 130, 700, 5000))
 def test_one_group_with_few_and_with_many_tiles(mode, rows):
@@ -175,8 +185,13 @@ def test_fused_relu2(counts):
 @pytest.mark.parametrize("counts", ([10, 0, 3, 50], [400, 0, 77, 1100]), ids=("few", "many"))
 def test_weight_gradient_in_32_bits_and_accumulated(counts):
     run("wgrad", counts, K=264, N=190, dtype="bf16", f32=True)
+    for K, N in ((100, 52), (1300, 1100)):  # single CTAs, CTA pairs
+        accumulated(counts, K, N)
+
+
+def accumulated(counts, K, N):
     gen = torch.Generator(device="cuda").manual_seed(3)
-    E, K, N, rows = len(counts), 100, 52, sum(counts)
+    E, rows = len(counts), sum(counts)
     off = offsets(counts)
     x, dy = padded((rows, K), torch.float16, gen), padded((rows, N), torch.float16, gen)
     dw = torch.randn(E, N, K, device="cuda", generator=gen)
