@@ -763,8 +763,8 @@ moe_status dispatch(GroupedArgs& a, const Operand& A, const Operand& B, bool out
     if (nb == 256 && tiles(2, 256) < sms / 2) nb = 128;
     if (nb == 128 && tiles(2, 128) < sms / 2) nb = 64;
     if (nb == 64) return run_variant<M, 1, 64, 2, 4, 2>(a, A, B, dev, sms, stream);
-    if (nb == 128) return run_variant<M, 2, 128, 2, 4, 2>(a, A, B, dev, sms, stream);
-    return run_variant<M, 2, 256, 2, 3, 2>(a, A, B, dev, sms, stream);
+    if (nb == 128) return run_variant<M, 2, 128, 1, 8, 2>(a, A, B, dev, sms, stream);
+    return run_variant<M, 2, 256, 1, 6, 2>(a, A, B, dev, sms, stream);
   } else {
     // small gradients: single CTAs and 128 x 128 tiles, four times as many
     const bool few = tiles(2, 256) < sms / 2;

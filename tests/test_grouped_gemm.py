@@ -159,6 +159,18 @@ def test_ragged_groups_with_many_tiles(mode, K, N, dtype):
         run(mode, [700, 0, 90, 1030, 256, 257], K=K, N=N, dtype=dtype, f32=True)
 
 
+@pytest.mark.parametrize("K,N", ((2040, 1992), (1999, 2001), (64, 4100)))
+@pytest.mark.parametrize("mode", ("fwd", "dgrad"))
+def test_groups_just_above_256_rows(mode, K, N):
+    # groups that fit one wide tile beside groups that do not; neighbouring tiles that fit the
+    # accumulators together, and that do not
+    for seed, counts in enumerate(([257, 320, 300, 0, 321, 289, 272, 256, 1, 255, 513, 304],
+                                   [320] * 12, [257, 255] * 8, [304, 17, 31, 33] + [318] * 9)):
+        avg = sum(counts) / len(counts)
+        assert 200 < avg <= 320
+        run(mode, counts, K=K, N=N, dtype="bf16", relu2=mode == "fwd", start=1, tail=1, seed=seed)
+
+
 @pytest.mark.parametrize("mode", MODES)
 @pytest.mark.parametrize("rows", (1, 130, 700, 5000))
 def test_one_group_with_few_and_with_many_tiles(mode, rows):
