@@ -287,7 +287,11 @@ typedef enum {
  *   ld*: elements from one row to the next, at least the row's width.
  *     Operands (x, dy, w): a multiple of 8; outputs: any.
  *   dtype: MOE_DTYPE_BF16 or MOE_DTYPE_FP16, of all operands and (except
- *     out_dtype) of the output.  Sums are float32, rounded once.
+ *     out_dtype) of the output.  Sums are float32, rounded once.  (The tensor
+ *     cores truncate as they add: a sum of q products loses about q * 1e-9 of
+ *     itself.  FP32 gradients are added up in pieces of 768 rows, which keeps
+ *     them within 1e-6.)
+ *   All pointers belong to the current device.
  *   status: optional device int32, OR-ed into (the caller zeroes it): bit 2
  *     if an entry of off is negative, falls below its predecessor or lies
  *     beyond `rows` (the group it starts or ends counts as empty, its
@@ -349,6 +353,7 @@ MOE_API moe_status moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const vo
  *      inputs; w_scale2 [E] float32.
  *   y  [num_tokens * k, N] of x's type, ldy elements apart.
  *   activation: MOE_ACT_NONE or MOE_ACT_RELU2.
+ *   All pointers belong to the current device.
  *   status: optional device int32, OR-ed into (the caller zeroes it): bit 2
  *      for an id outside [0, num_experts), bit 1 if a wait timed out.
  * Weights and scales are exact, an element of x counts to 2^-22 of its row's

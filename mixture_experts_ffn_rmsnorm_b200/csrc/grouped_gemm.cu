@@ -92,6 +92,11 @@ struct Traits {
   static constexpr int kRound = M == kWgrad && EB == 2 ? 2 : 1;
   static constexpr int kWarpStaging = kRound * kChunk;
   static constexpr int kStagingBytes = kEpiWarps * kWarpStaging;
+  // The tensor cores truncate as they accumulate: a sum of n rows loses about
+  // n * 1e-9 of itself (measured: 9e-6 at 8192).  A 16-bit result hides that;
+  // for an FP32 one the sums start anew every 768 rows (7e-7) and are added up
+  // by the epilogue, rounding to nearest.
+  static constexpr int kSegment = EB == 4 ? 12 : 1 << 30;  // k-blocks
   static constexpr int kSmem = 1024 + STAGES * kStageBytes + kStagingBytes + 512;
   static_assert(!kBMN || KPS == 1, "the tail of a group is one k-block of one stage");
   static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols <= 512, "");
@@ -262,9 +267,10 @@ __device__ __forceinline__ void stage_chunk_32(const uint32_t (&acc)[32], uint32
 }
 
 // The same without staging: a warp's store of one r is 128 contiguous bytes.
+// (add: the elements are this lane's alone, in every segment of a sum.)
 __device__ __forceinline__ void store_chunk_32(const GroupedArgs& p, const uint32_t (&acc)[32],
-                                               float* o, int n) {
-  if (p.accumulate) {
+                                               float* o, int n, bool add) {
+  if (add) {
     float old[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) old[j] = j < n ? o[j * p.ldo] : 0.f;
@@ -453,48 +459,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nk = uniform(walk.t.nk), nr = uniform(walk.t.nr), cnt = uniform(walk.t.cnt);
         if (nk == 0) continue;
         const uint32_t idesc = make_idesc_16(128 * CG, (nr + 15) & ~15, p.fmt, Tr::kAMN, Tr::kBMN);
-        const int ab = it & 1;
-        ok = uniform(mbar_wait(&tempty[ab], ((it >> 1) & 1) ^ 1u, abort));
-        if (!ok) break;
-        ++it;
-        tc_fence_after();
-        const uint32_t d = tmem_base + uint32_t(ab * NB);
         const int last = (cnt - (nk - 1) * kBK + 15) / 16;  // weight gradient: steps with rows
-        for (int kb0 = 0; kb0 < nk; kb0 += KPS) {
-          // a group's last k-block: the pair's warps 2 may have written to it
-          const bool is_tail = M == kWgrad && kb0 + 1 == nk && (cnt & 15) != 0;
-          ok = uniform(CG == 2 && is_tail ? mbar_wait_acquire_cluster(&full[stage], phase, abort)
-                                          : mbar_wait(&full[stage], phase, abort));
+        for (int seg = 0; seg < nk && ok; seg += Tr::kSegment) {
+          const int end = Tr::kSegment < nk - seg ? seg + Tr::kSegment : nk;
+          const int ab = it & 1;
+          ok = uniform(mbar_wait(&tempty[ab], ((it >> 1) & 1) ^ 1u, abort));
           if (!ok) break;
+          ++it;
           tc_fence_after();
-          const int kbn = min(KPS, nk - kb0);
-          const uint32_t sa0 = tiles_u32 + stage * Tr::kStageBytes;
-          if (elect_one()) {
+          const uint32_t d = tmem_base + uint32_t(ab * NB);
+          for (int kb0 = seg; kb0 < end; kb0 += KPS) {
+            // a group's last k-block: the pair's warps 2 and 3 may have written to it
+            const bool is_tail = M == kWgrad && kb0 + 1 == nk && (cnt & 15) != 0;
+            ok = uniform(CG == 2 && is_tail ? mbar_wait_acquire_cluster(&full[stage], phase, abort)
+                                            : mbar_wait(&full[stage], phase, abort));
+            if (!ok) break;
+            tc_fence_after();
+            const int kbn = min(KPS, nk - kb0);
+            const uint32_t sa0 = tiles_u32 + stage * Tr::kStageBytes;
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < KPS; ++kk) {
-              if (kk >= kbn) break;
-              const uint32_t sa = sa0 + kk * (Tr::kABytes + Tr::kBBytes), sb = sa + Tr::kABytes;
-              const uint64_t ad =
-                  Tr::kAMN ? smem_desc_mn_sw128(sa, 8192) : smem_desc_k_sw128(sa);
-              const uint64_t bd =
-                  Tr::kBMN ? smem_desc_mn_sw128(sb, 8192) : smem_desc_k_sw128(sb);
-              const int ks = M == kWgrad && kb0 + 1 == nk ? last : kBK / 16;
+              for (int kk = 0; kk < KPS; ++kk) {
+                if (kk >= kbn) break;
+                const uint32_t sa = sa0 + kk * (Tr::kABytes + Tr::kBBytes), sb = sa + Tr::kABytes;
+                const uint64_t ad =
+                    Tr::kAMN ? smem_desc_mn_sw128(sa, 8192) : smem_desc_k_sw128(sa);
+                const uint64_t bd =
+                    Tr::kBMN ? smem_desc_mn_sw128(sb, 8192) : smem_desc_k_sw128(sb);
+                const int ks = M == kWgrad && kb0 + 1 == nk ? last : kBK / 16;
 #pragma unroll
-              for (int s = 0; s < kBK / 16; ++s)
-                if (M != kWgrad || s < ks)
-                  umma_f16_cg<CG>(d, ad + s * (Tr::kAMN ? 128 : 2), bd + s * (Tr::kBMN ? 128 : 2),
-                                  idesc, (kb0 | kk | s) ? 1u : 0u);
+                for (int s = 0; s < kBK / 16; ++s)
+                  if (M != kWgrad || s < ks)
+                    umma_f16_cg<CG>(d, ad + s * (Tr::kAMN ? 128 : 2),
+                                    bd + s * (Tr::kBMN ? 128 : 2), idesc,
+                                    (kb0 - seg) | kk | s ? 1u : 0u);
+              }
+              umma_commit_cg<CG>(&empty[stage]);
             }
-            umma_commit_cg<CG>(&empty[stage]);
+            __syncwarp();
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
+          if (ok && elect_one()) umma_commit_cg<CG>(&tfull[ab]);
           __syncwarp();
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-        if (ok && elect_one()) umma_commit_cg<CG>(&tfull[ab]);
-        __syncwarp();
       }
       if (!ok && lane == 0) give_up(p, abort);
       // every MMA issued has completed once `drain` flips (in both CTAs)
@@ -546,91 +556,96 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = (warp - 4) >> 2;  // chunks of 32 r's: even or odd ones
     const uint32_t st = smem_u32(staging) + (warp - 4) * Tr::kWarpStaging;
     int it = 0;
-    while (uniform(walk.next(p, s_rows, s_pre))) {
+    bool ok = true;
+    while (ok && uniform(walk.next(p, s_rows, s_pre))) {
       const int nk = uniform(walk.t.nk), nr = uniform(walk.t.nr), r0 = uniform(walk.t.r0);
       const int e = uniform(walk.t.e);
       const int cw = uniform(walk.t.c0) + int(rank) * 128 + q * 32;
       const long long row = M == kWgrad ? r0 : (long long)(uniform(walk.t.row0)) + r0;
       const long long base = (M == kWgrad ? e * p.group_stride : 0) + row * p.ldo;
-      const int ab = it & 1;
-      if (nk > 0) {
-        if (!uniform(mbar_wait(&tfull[ab], (it >> 1) & 1, abort))) {
-          if (lane == 0) give_up(p, abort);
-          break;
+      for (int seg = 0; seg == 0 || (seg < nk && ok); seg += Tr::kSegment) {
+        const int ab = it & 1;
+        if (nk > 0) {
+          if (!uniform(mbar_wait(&tfull[ab], (it >> 1) & 1, abort))) {
+            if (lane == 0) give_up(p, abort);
+            ok = false;
+            break;
+          }
+          ++it;
+          tc_fence_after();
         }
-        ++it;
-        tc_fence_after();
-      }
-      const uint32_t tb = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(ab * NB);
-      const bool mine = cw < p.C;  // the warp has c's to store
+        const uint32_t tb = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(ab * NB);
+        const bool mine = cw < p.C;  // the warp has c's to store
 #pragma unroll 1
-      for (int j0 = half * 32 * Tr::kRound; j0 < nr && mine; j0 += 64 * Tr::kRound) {
-        // the bulk store of the round before has read the staging tile
-        const bool bulk = M == kWgrad && p.tma_out;
-        if (bulk) {
-          if (elect_one()) bulk_wait_read<0>();
-          __syncwarp();
-        }
-        if constexpr (EB == 4) {
-          uint32_t r[32];
-          if (nk > 0) {
-            tmem_ld_32x32b_x32(tb + uint32_t(j0), r);
-            tmem_ld_wait();
-          } else {  // an empty group's gradient
-#pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = 0u;
-          }
-          if (bulk)
-            stage_chunk_32(r, st);
-          else if (cw + lane < p.C)
-            store_chunk_32(p, r, static_cast<float*>(p.out) + base + j0 * p.ldo + cw + lane,
-                           nr - j0);
-        } else {
-          uint32_t r[2 * Tr::kRound][16];
-          if (nk > 0) {
-#pragma unroll
-            for (int c = 0; c < Tr::kRound; ++c) {
-              tmem_ld_16x256b_x4(tb + uint32_t(j0 + 32 * c), r[2 * c]);
-              tmem_ld_16x256b_x4(tb + (16u << 16) + uint32_t(j0 + 32 * c), r[2 * c + 1]);
-            }
-            tmem_ld_wait_regs(r);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 2 * Tr::kRound; ++c)
-#pragma unroll
-              for (int j = 0; j < 16; ++j) r[c][j] = 0u;
-          }
-#pragma unroll
-          for (int c = 0; c < Tr::kRound; ++c)
-            stage_chunk_16(p, r[2 * c], r[2 * c + 1], st + c * Tr::kChunk);
-          if (!bulk) {
+        for (int j0 = half * 32 * Tr::kRound; j0 < nr && mine; j0 += 64 * Tr::kRound) {
+          // the bulk store of the round before has read the staging tile
+          const bool bulk = M == kWgrad && p.tma_out && nk <= Tr::kSegment;
+          if (bulk) {
+            if (elect_one()) bulk_wait_read<0>();
             __syncwarp();
+          }
+          if constexpr (EB == 4) {
+            uint32_t r[32];
+            if (nk > 0) {
+              tmem_ld_32x32b_x32(tb + uint32_t(j0), r);
+              tmem_ld_wait();
+            } else {  // an empty group's gradient
+#pragma unroll
+              for (int j = 0; j < 32; ++j) r[j] = 0u;
+            }
+            if (bulk)
+              stage_chunk_32(r, st);
+            else if (cw + lane < p.C)
+              store_chunk_32(p, r, static_cast<float*>(p.out) + base + j0 * p.ldo + cw + lane,
+                             nr - j0, p.accumulate || seg > 0);
+          } else {
+            uint32_t r[2 * Tr::kRound][16];
+            if (nk > 0) {
+#pragma unroll
+              for (int c = 0; c < Tr::kRound; ++c) {
+                tmem_ld_16x256b_x4(tb + uint32_t(j0 + 32 * c), r[2 * c]);
+                tmem_ld_16x256b_x4(tb + (16u << 16) + uint32_t(j0 + 32 * c), r[2 * c + 1]);
+              }
+              tmem_ld_wait_regs(r);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 2 * Tr::kRound; ++c)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) r[c][j] = 0u;
+            }
 #pragma unroll
             for (int c = 0; c < Tr::kRound; ++c)
-              store_chunk_16(p, st + c * Tr::kChunk,
-                             static_cast<uint16_t*>(p.out) + base + (j0 + 32 * c) * p.ldo, cw,
-                             nr - j0 - 32 * c);
+              stage_chunk_16(p, r[2 * c], r[2 * c + 1], st + c * Tr::kChunk);
+            if (!bulk) {
+              __syncwarp();
+#pragma unroll
+              for (int c = 0; c < Tr::kRound; ++c)
+                store_chunk_16(p, st + c * Tr::kChunk,
+                               static_cast<uint16_t*>(p.out) + base + (j0 + 32 * c) * p.ldo, cw,
+                               nr - j0 - 32 * c);
+              __syncwarp();
+            }
+          }
+          if (bulk) {
+            fence_proxy_async_smem();
             __syncwarp();
+            if (elect_one()) {
+              tma_store_3d(&p.tmO, st, cw, r0 + j0, e);
+              bulk_commit();
+            }
           }
         }
-        if (bulk) {
-          fence_proxy_async_smem();
+        if (nk > 0) {
+          tc_fence_before();
           __syncwarp();
-          if (elect_one()) {
-            tma_store_3d(&p.tmO, st, cw, r0 + j0, e);
-            bulk_commit();
+          if (lane == 0) {
+            if (CG == 2)
+              mbar_arrive_at(map_to_rank(smem_u32(&tempty[ab]), 0));
+            else
+              mbar_arrive(&tempty[ab]);
           }
         }
-      }
-      if (nk > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (CG == 2)
-            mbar_arrive_at(map_to_rank(smem_u32(&tempty[ab]), 0));
-          else
-            mbar_arrive(&tempty[ab]);
-        }
+        if (Tr::kSegment >= nk) break;
       }
     }
     if (M == kWgrad && elect_one()) bulk_wait_all();
@@ -763,11 +778,12 @@ moe_status dispatch(GroupedArgs& a, const Operand& A, const Operand& B, bool out
   };
   if constexpr (M != kWgrad) {
     // The row tile that covers an average group, and a smaller one where the
-    // tiles would leave SMs idle.  128 groups of K = 2688, N = 1856, forward:
-    // 1 / 48 / 64 rows 188 / 203 / 205 us with 64-row tiles, 207 / 238 / 239
-    // with 256 (64 KB of weights under way a CTA, not 48); 96 / 128 rows 219 /
-    // 229 us with 128-row tiles, 345 / 311 with 64, 244 / 281 with 256; 200
-    // rows 277 us with 256, 351 with 128.
+    // tiles would leave SMs idle.  128 groups of K = 2688, N = 1856, forward,
+    // with row tiles of 64 / 128 / 256: 1 row a group 184 / 188 / 195 us, 48
+    // 206 / 209 / 216, 64 213 / 214 / 224, 80 282 / 226 / 234, 128 311 / 254 /
+    // 260, 160 413 / 338 / 295, 256 553 / 420 / 357.  One group of 2048 rows,
+    // K = 1024, N = 512: 6.9 us with 64-row tiles, 11.3 with 256; 8192 rows, N =
+    // 1024: 17.6 with 256 (132 tiles for 74 pairs).
     int nb = a.rows <= 64LL * a.groups ? 64 : a.rows <= 128LL * a.groups ? 128 : 256;
     if (nb == 256 && tiles(2, 256) < sms / 2) nb = 128;
     if (nb == 128 && tiles(2, 128) < sms / 2) nb = 64;
@@ -775,7 +791,9 @@ moe_status dispatch(GroupedArgs& a, const Operand& A, const Operand& B, bool out
     if (nb == 128) return run_variant<M, 2, 128, 1, 8, 2>(a, A, B, dev, sms, stream);
     return run_variant<M, 2, 256, 1, 6, 2>(a, A, B, dev, sms, stream);
   } else {
-    // small gradients: single CTAs and 128 x 128 tiles, four times as many
+    // Small gradients: single CTAs and 128 x 128 tiles, four times as many (one
+    // group of 571 rows, K = 856, N = 768: 8.0 us for 10.4; two of 200 rows,
+    // 376 x 872: 7.1 for 9.2).
     const bool few = tiles(2, 256) < sms / 2;
     if (out_f32)
       return few ? run_variant<M, 1, 128, 1, 5, 4>(a, A, B, dev, sms, stream)

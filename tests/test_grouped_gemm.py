@@ -215,6 +215,23 @@ def accumulated(counts, K, N):
     assert torch.equal(dw[1], before[1])  # nothing to add to an empty group
 
 
+@pytest.mark.parametrize("rows,K,N", ((8192, 512, 512), (8191, 2048, 2304), (769, 96, 40)))
+def test_long_sums_in_32_bits(rows, K, N):
+    # Every addition of a k-step truncates by less than an ulp (2^-23) of the partial sum.  Sums of
+    # random signs grow as the square root of their length, so 48 steps lose less than
+    # 48 * 2/3 * 2^-23 = 3.9e-6 of the result in the 2-norm; without a fresh start every 768 rows the
+    # 512 steps of 8192 rows could lose 4.1e-5 (and lost 9.1e-6).
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    x, dy = padded((rows, K), torch.bfloat16, gen), padded((rows, N), torch.bfloat16, gen)
+    dw = torch.full((1, N, K), 7.0, device="cuda")
+    moe.grouped_gemm_wgrad(dy, x, offsets([rows]), dw)
+    ref = dy.double().T @ x.double()
+    assert (dw[0].double() - ref).norm() <= 3.9e-6 * ref.norm()
+    moe.grouped_gemm_wgrad(dy, x, offsets([rows]), dw, accumulate=True)
+    assert (dw[0].double() - 2 * ref).norm() <= 3.9e-6 * 2 * ref.norm()
+    run("wgrad", [rows - 700, 0, 700], K=K, N=N, dtype="bf16", f32=True)
+
+
 @pytest.mark.parametrize("f32", (False, True))
 @pytest.mark.parametrize("blocks", (1, 2, 4, 5, 6))
 def test_tails_of_neighbouring_tiles_in_one_stage(blocks, f32):
