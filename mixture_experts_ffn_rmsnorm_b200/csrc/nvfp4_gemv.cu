@@ -38,6 +38,10 @@
 //              tcgen05.cp, the four copies of a stage held up its MMAs);
 //   warps 12-19 the token rows' digits, a pass ahead of its MMAs.
 // Results do not depend on the grid.
+//
+// Measured (one B200, graph replay): one token, six experts of 2688 x 1856, 8.5
+// us (17 MB; launch 2.2 us, passes, digits and the MMAs of one tile follow one
+// another); 8 tokens, about 39 experts of 1856 x 2688, 25 us (4.6 TB/s).
 #include <cuda_fp16.h>
 
 #include "handle_free.h"
