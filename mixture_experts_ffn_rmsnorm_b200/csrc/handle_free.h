@@ -61,6 +61,23 @@ inline EncodeTiledFn encode_tiled() {
   return fn;
 }
 
+// Encodes a map.  The driver's call wants a current context, which a host
+// thread has only once a runtime call bound the device's primary one to it:
+// without one, bind it and try again.
+template <typename F>
+inline bool encode_bound(const F& encode) {
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) {
+      cudaGetLastError();
+      return false;
+    }
+    r = encode();
+  }
+  return r == CUDA_SUCCESS;
+}
+
 // 3-D map of a row-major tensor [groups, rows, inner]: box = one swizzle span
 // (128 bytes, or 64) of the inner extent x box_rows rows of one group; loads
 // zero-fill beyond each extent, stores leave it out.  Strides in bytes,
@@ -75,28 +92,12 @@ inline bool make_map_3d(CUtensorMap* m, CUtensorMapDataType type, uint32_t elem_
   const cuuint64_t strides[2] = {row_stride, group_stride};
   const cuuint32_t box[3] = {span / elem_bytes, box_rows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, type, 3, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE,
-             span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// 3-D map of a byte matrix [rows, blocks * 128] as [blocks, rows, 128]: one
-// box = 16 rows x up to `blocks` (at most 256) spans of 128 bytes, each span
-// a tile of its own in shared memory (128-byte swizzle).
-inline bool make_map_spans(CUtensorMap* m, const void* base, uint64_t rows, uint64_t row_stride,
-                           uint32_t blocks, uint32_t box_rows) {
-  const EncodeTiledFn enc = encode_tiled();
-  if (!enc) return false;
-  const cuuint64_t dims[3] = {128, rows, blocks};
-  const cuuint64_t strides[2] = {row_stride, 128};
-  const cuuint32_t box[3] = {128, box_rows, blocks};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_bound([&] {
+    return enc(m, type, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE,
+               span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
 }
 
 }  // namespace moe

@@ -9,6 +9,8 @@ d = q * 2^-23 * S, where S is the sum of the products' magnitudes.  relu^2
 of a sum off by d is off by at most 2 |s| d + d^2.  One rounding to the output
 type adds half a step: eps / 2 of the value (plus half the smallest subnormal).
 """
+from concurrent.futures import ThreadPoolExecutor
+
 import numpy as np
 import pytest
 
@@ -358,6 +360,111 @@ def test_captured_and_replayed_beside_another_stream():
             ref, mag = reference(mode, t["off"], E, t["dy"], t["x"], t["w"])
             check(t[name], *bound(ref, mag, q, t[name].dtype), name)
         t["graph"].reset()
+
+
+def test_streams_that_join_inside_one_capture():
+    # forward and weight gradient on two streams forked from the capturing one, the data gradient
+    # after the join; each launch has dependencies on other streams
+    gen = torch.Generator(device="cuda").manual_seed(21)
+    E, K, N = 5, 328, 264
+    counts = [700, 3, 0, 64, 257]
+    rows = sum(counts)
+    off, off0 = offsets(counts), offsets(counts)
+    x, dy = padded((rows, K), torch.bfloat16, gen), padded((rows, N), torch.bfloat16, gen)
+    w = padded((E, N, K), torch.bfloat16, gen)
+    y = torch.zeros(rows, N, dtype=torch.bfloat16, device="cuda")
+    dx = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    dw = torch.zeros(E, N, K, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        off.copy_(off0)
+        side.wait_stream(here)
+        moe.grouped_gemm(x, w, off, y)
+        with torch.cuda.stream(side):
+            moe.grouped_gemm_wgrad(dy, x, off, dw)
+        here.wait_stream(side)
+        moe.grouped_gemm_dgrad(y, w, off, dx)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in range(3):
+        off0.copy_(offsets([100, 300, 24, 600, 0]))
+        x.copy_(torch.randn(rows, K, device="cuda", generator=gen))
+        for t in (y, dx, dw, off):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for mode, out, q in (("fwd", y, K), ("dgrad", dx, N), ("wgrad", dw, 600)):
+            ref, mag = reference(mode, off0, E, y if mode == "dgrad" else dy, x, w)
+            check(out, *bound(ref, mag, q, out.dtype), (mode, seed))
+    graph.reset()
+
+
+def test_threads_at_once():
+    # two host threads, a stream each, the same weights; every result is the lone call's, bit by bit
+    gen = torch.Generator(device="cuda").manual_seed(22)
+    E, K, N = 6, 512, 328
+    counts = [300, 0, 1, 47, 600, 64]
+    rows, off = sum(counts), offsets(counts)
+    w = padded((E, N, K), torch.bfloat16, gen)
+    xs = [padded((rows, K), torch.bfloat16, gen) for _ in range(2)]
+    dys = [padded((rows, N), torch.bfloat16, gen) for _ in range(2)]
+
+    def outputs():
+        return (torch.zeros(rows, N, dtype=torch.bfloat16, device="cuda"),
+                torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda"),
+                torch.zeros(E, N, K, device="cuda"))
+
+    def calls(i, out, stream):
+        moe.grouped_gemm(xs[i], w, off, out[0], stream=stream)
+        moe.grouped_gemm_dgrad(dys[i], w, off, out[1], stream=stream)
+        moe.grouped_gemm_wgrad(dys[i], xs[i], off, out[2], stream=stream)
+
+    alone = [outputs() for _ in range(2)]
+    for i in range(2):
+        calls(i, alone[i], None)
+    many = [[outputs() for _ in range(8)] for _ in range(2)]
+    torch.cuda.synchronize()
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        for out in many[i]:
+            calls(i, out, stream)
+        stream.synchronize()
+
+    with ThreadPoolExecutor(2) as pool:
+        for f in [pool.submit(work, i) for i in range(2)]:
+            f.result()
+    for i in range(2):
+        for out in many[i]:
+            assert all(torch.equal(a, b) for a, b in zip(alone[i], out))
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("K,N", ((131072, 8), (8, 131072)))
+def test_widest_matrices(mode, K, N):
+    run(mode, [5, 0, 70], K, N, "bf16")
+
+
+@pytest.mark.parametrize("mode", ("fwd", "dgrad"))
+def test_most_rows(mode):
+    # 2^24 rows of 8 elements: the largest row numbers, in the last groups
+    rows, K, N = 1 << 24, 8, 8
+    gen = torch.Generator(device="cuda").manual_seed(23)
+    a = torch.randint(-3, 4, (rows, 8), device="cuda", generator=gen).to(torch.bfloat16)
+    w = torch.randint(-3, 4, (3, N, K), device="cuda", generator=gen).to(torch.bfloat16)
+    off = offsets([rows - 1000, 999, 1])
+    out = torch.full((rows, 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    (moe.grouped_gemm if mode == "fwd" else moe.grouped_gemm_dgrad)(a, w, off, out)
+    # whole numbers of magnitude at most 72: exact in bfloat16
+    for e, (lo, hi) in enumerate(((0, rows - 1000), (rows - 1000, rows - 1), (rows - 1, rows))):
+        m = w[e].float().T if mode == "fwd" else w[e].float()
+        assert torch.equal(out[lo:hi].float(), (a[lo:hi, :, None].float() * m).sum(1)), e
 
 
 def test_gradients_against_differences():

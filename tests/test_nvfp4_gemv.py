@@ -13,6 +13,8 @@ float32 and rounding the result to its type add half a step each (2^-24 and eps 
 the value, and half the smallest subnormal of the type); relu^2 of a value off by d is
 off by at most 2 |v| d + d^2.
 """
+from concurrent.futures import ThreadPoolExecutor
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -234,6 +236,24 @@ def test_captured_replayed_and_deterministic():
     check(out[0], *expected(x, idx, w, s, s2, False, y.dtype))
     assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
     graph.reset()
+
+
+def test_first_call_of_a_thread():
+    # a host thread that has made no CUDA call yet, and one beside it
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    E, N, K, T, k = 16, 100, 320, 4, 3
+    w, s, s2 = weights(E, N, K, gen)
+    x = torch.randn(T, K, device="cuda", generator=gen).to(torch.bfloat16)
+    idx = torch.rand(T, E, device="cuda", generator=gen).topk(k, dim=1).indices.to(torch.int32)
+    ys = torch.zeros(3, T, k, N, dtype=torch.bfloat16, device="cuda")
+    moe.nvfp4_gemv(x, idx, w, s, s2, ys[2])
+    check(ys[2], *expected(x, idx, w, s, s2, False, ys.dtype))
+    torch.cuda.synchronize()
+    with ThreadPoolExecutor(2) as pool:
+        for f in [pool.submit(moe.nvfp4_gemv, x, idx, w, s, s2, ys[i]) for i in range(2)]:
+            f.result()
+    torch.cuda.synchronize()
+    assert torch.equal(ys[0], ys[2]) and torch.equal(ys[1], ys[2])
 
 
 def test_refusals():
