@@ -277,7 +277,7 @@ def grouped_gemm_wgrad(dy, x, off, dw, accumulate=False, status=None, stream=Non
     rows = dy.shape[0]
     if dy.shape[1] != N or x.shape != (rows, K):
         raise MoEError(1, f"{what}: shapes {tuple(dy.shape)}, {tuple(x.shape)}, {tuple(dw.shape)}")
-    dt = _dtype_code(dy, what)
+    dt, odt = _dtype_code(dy, what), _dtype_code(dw, what)
     if x.dtype != dy.dtype:
         raise MoEError(1, f"{what}: dy and x have different dtypes")
     _check_off(off, E, what)
@@ -285,7 +285,7 @@ def grouped_gemm_wgrad(dy, x, off, dw, accumulate=False, status=None, stream=Non
     s = _launch_stream(what, stream, dy, x, off, dw, status)
     st = (_lib or load_library()).moe_grouped_gemm_wgrad(
         dy.data_ptr(), ldy, x.data_ptr(), ldx, off.data_ptr(), E, rows, K, N, dt, dw.data_ptr(),
-        ldw, _dtype_code(dw, what), int(accumulate), _ptr(status), s)
+        ldw, odt, int(accumulate), _ptr(status), s)
     if st != 0:
         raise MoEError(st, what)
 

@@ -204,3 +204,49 @@ def test_nvfp4_gemv_validates_on_host():
     assert gemv(T=-1) == 4
     assert gemv(T=342) == 4  # 1026 routed rows
     assert gemv(T=0, x=None, y=None) == 0
+
+
+def refused(code, f, *a, **kw):
+    with pytest.raises(moe.MoEError) as ei:
+        f(*a, **kw)
+    assert ei.value.status == code
+
+
+def test_grouped_gemm_wrappers_refuse_bad_tensors():
+    torch = pytest.importorskip("torch")
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt)  # noqa: E731
+    off = torch.zeros(3, dtype=torch.int32)
+    x, w, y, dw = z(8, 64), z(2, 48, 64), z(8, 48), z(2, 48, 64)
+    for f, a in ((moe.grouped_gemm, (x, w, off, y)), (moe.grouped_gemm_dgrad, (y, w, off, x)),
+                 (moe.grouped_gemm_wgrad, (y, x, off, dw))):
+        refused(7, f, *a)  # good shapes, but not on the device
+        for i in range(4):
+            flat = list(a)
+            flat[i] = flat[i].reshape(-1)[:-1]
+            refused(1, f, *flat)
+        refused(1, f, a[0].double(), *a[1:])
+        refused(1, f, a[0], a[1].half(), *a[2:])
+        refused(1, f, *a[:2], off.long(), a[3])
+        refused(1, f, *a[:3], a[3].double())
+        refused(1, f, *a, status=z(1))
+        refused(1, f, a[0][:7], *a[1:])
+    refused(1, moe.grouped_gemm, x, z(1, 48, 64).expand(2, 48, 64), off, y)  # one matrix for all
+    refused(1, moe.grouped_gemm, x, w.transpose(1, 2), off, z(8, 64))
+    refused(1, moe.grouped_gemm, z(64, 8).T, w, off, y)
+
+
+def test_nvfp4_gemv_wrapper_refuses_bad_tensors():
+    torch = pytest.importorskip("torch")
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt)  # noqa: E731
+    good = [z(2, 64), z(2, 3, dt=torch.int32), z(4, 24, 32, dt=torch.uint8),
+            z(4, 24, 4, dt=torch.uint8), z(4, dt=torch.float32), z(2, 3, 24)]
+    refused(7, moe.nvfp4_gemv, *good)  # good shapes, but not on the device
+    bad = [(0, z(2, 32)), (0, z(2, 1, 64)), (0, z(64)), (0, z(2, 64, dt=torch.float64)),
+           (1, z(2, 3, dt=torch.int64)), (1, z(6, dt=torch.int32)),
+           (2, z(4, 24, 32, dt=torch.int8)), (2, z(24, 32, dt=torch.uint8)),
+           (2, z(4, 24, 64, dt=torch.uint8)[..., :32]), (3, z(4, 24, 3, dt=torch.uint8)),
+           (3, z(4, 24, 4)), (4, z(3, dt=torch.float32)), (4, z(4)), (5, z(2, 3, 25)),
+           (5, z(2, 3, 24, dt=torch.float16)), (5, z(6, 24))]
+    for i, t in bad:
+        refused(1, moe.nvfp4_gemv, *good[:i], t, *good[i + 1:])
+    refused(1, moe.nvfp4_gemv, *good, status=z(1))
