@@ -97,11 +97,30 @@ struct Traits {
   // for an FP32 one the sums start anew every 768 rows (7e-7) and are added up
   // by the epilogue, rounding to nearest.
   static constexpr int kSegment = EB == 4 ? 12 : 1 << 30;  // k-blocks
-  static constexpr int kSmem = 1024 + STAGES * kStageBytes + kStagingBytes + 512;
+  // Weight gradient: a group's last k-block is loaded this many k-blocks ahead of
+  // its turn, in which time the rows behind the group's last one are cleared
+  // (128 groups of 500 / 333 / 261 / 135 rows, 2688 x 1856, us: 0 ahead 805 / 573
+  // / 511 / 361, 2 ahead 773 / 565 / 495 / 365; with five stages instead of six
+  // 0 ahead 807 / 624 / 520 / 380, 3 ahead 784 / 619 / 550 / 380).
+  static constexpr int kAhead = 2;
+  static_assert(M != kWgrad || kAhead < STAGES, "");
+  // behind the stages and the staging tiles: barriers, the groups' bounds, row
+  // tiles before each group, a scan's sums
+  static constexpr int kBarriers = (4 * STAGES + 6) * 8;
+  static constexpr int kSmem = STAGES * kStageBytes + kStagingBytes + kBarriers +
+                               (2 * (MOE_MAX_EXPERTS + 1) + kThreads / 32) * 4;
   static_assert(!kBMN || KPS == 1, "the tail of a group is one k-block of one stage");
   static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols <= 512, "");
-  static_assert(kSmem <= 232448 - 8192, "");  // beside the static tables
+  static_assert(kSmem <= 232448, "");
 };
+
+// Weight gradient: place in the order of a tile's loads of the k-block that has
+// rows to clear (nk: there is none).  The others keep their order.
+template <typename Tr>
+__device__ __forceinline__ int tail_place(int nk, int cnt) {
+  if ((cnt & 15) == 0) return nk;  // whole steps of 16 rows
+  return max(nk - 1 - Tr::kAhead, (nk - 1) / Tr::kSegment * Tr::kSegment);
+}
 
 struct GTile {
   int e;
@@ -135,8 +154,8 @@ struct Walk {
 
   __device__ __forceinline__ void group(const GroupedArgs& p, const int* off, int g) {
     t.e = g;
-    t.row0 = off[2 * g];
-    t.cnt = off[2 * g + 1];
+    t.row0 = off[g];
+    t.cnt = off[g + 1] - t.row0;
     t.nk = ((M == kWgrad ? t.cnt : p.Q) + kBK - 1) / kBK;
   }
 
@@ -288,9 +307,7 @@ template <Mode M, int CG, int NB, int KPS, int STAGES, int EB>
 __global__ void __launch_bounds__(kThreads, 1)
     ragged_gemm_kernel(const __grid_constant__ GroupedArgs p) {
   using Tr = Traits<M, CG, NB, KPS, STAGES, EB>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
-  uint8_t* tiles = smem_raw + pad;
+  extern __shared__ __align__(1024) uint8_t tiles[];
   uint8_t* staging = tiles + STAGES * Tr::kStageBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + Tr::kStagingBytes);
   uint64_t* empty = full + STAGES;
@@ -300,10 +317,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((4 * STAGES + 5) * 8 + 8 <= 512, "");
-  __shared__ int s_pre[MOE_MAX_EXPERTS + 1];
-  __shared__ int s_scan[kThreads / 32];
-  __shared__ int s_rows[2 * MOE_MAX_EXPERTS];  // {first row, rows} of each group
+  static_assert(Tr::kBarriers == (4 * STAGES + 5) * 8 + 8, "");
+  int* s_off = reinterpret_cast<int*>(full) + Tr::kBarriers / 4;  // groups' bounds
+  int* s_pre = s_off + MOE_MAX_EXPERTS + 1;
+  int* s_scan = s_pre + MOE_MAX_EXPERTS + 1;
 
   const int warp = uniform(int(threadIdx.x >> 5));
   const int lane = threadIdx.x & 31;
@@ -340,8 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool good = a >= 0 && a <= b && b <= p.rows;
       if (!good && p.status && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
       const int cnt = good ? b - a : 0;
-      s_rows[2 * e] = good ? a : 0;
-      s_rows[2 * e + 1] = cnt;
+      s_off[e] = a;
+      if (e + 1 == p.groups) s_off[p.groups] = b;
       n = ((M == kWgrad ? p.R : cnt) + NB - 1) / NB;
       if (M == kWgrad && cnt == 0 && p.accumulate) n = 0;  // nothing to add
       if (M == kWgrad && !good) n = 0;  // a bad group's gradient is left as it was
@@ -363,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  Walk<M, Tr::kTileC, NB> walk(p, s_rows, s_pre, int(blockIdx.x) / CG, int(gridDim.x) / CG);
+  Walk<M, Tr::kTileC, NB> walk(p, s_off, s_pre, int(blockIdx.x) / CG, int(gridDim.x) / CG);
   const uint32_t tiles_u32 = smem_u32(tiles);
 
   if (warp == 0) {
@@ -371,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0, tails = 0;
     uint32_t phase = 0;
     bool ok = true;
-    while (ok && uniform(walk.next(p, s_rows, s_pre))) {
+    while (ok && uniform(walk.next(p, s_off, s_pre))) {
       const int nk = uniform(walk.t.nk), nr = uniform(walk.t.nr), cnt = uniform(walk.t.cnt);
       const int e = uniform(walk.t.e), row0 = uniform(walk.t.row0), r0 = uniform(walk.t.r0);
       const int nmma = (nr + 15) & ~15;
@@ -390,12 +407,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         size = nb <= 16 ? 0 : nb <= 32 ? 1 : nb <= 64 ? 2 : 3;
         bbytes = 2048u << size;
       }
+      const int place = M == kWgrad ? tail_place<Tr>(nk, cnt) : nk;
       for (int kb0 = 0; kb0 < nk; kb0 += KPS) {
         ok = uniform(mbar_wait(&empty[stage], phase ^ 1u, abort));
         if (!ok) break;
         const int kbn = min(KPS, nk - kb0);
         const uint32_t bytes = uint32_t(kbn) * (Tr::kABytes + bbytes);
-        const bool is_tail = M == kWgrad && kb0 + 1 == nk && (cnt & 15) != 0;
+        const bool is_tail = M == kWgrad && kb0 == place;
+        const int first = M != kWgrad || kb0 < place ? kb0 : is_tail ? nk - 1 : kb0 - 1;
         const uint32_t st = tiles_u32 + stage * Tr::kStageBytes;
         if (elect_one()) {
           uint32_t bar;
@@ -413,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < KPS; ++kk) {
             if (kk >= kbn) break;
-            const int q = (kb0 + kk) * kBK;
+            const int q = (first + kk) * kBK;
             const uint32_t sa = st + kk * (Tr::kABytes + Tr::kBBytes), sb = sa + Tr::kABytes;
             if constexpr (M == kFwd) {
               tma_load_3d<CG>(sa, &p.tmA, bar, q, ca, e);
@@ -452,12 +471,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // about 180 cycles to issue, more than the 128 of its 256 x 256 x 16
     // product.
     if (rank == 0) {
-      int stage = 0, it = 0;
-      uint32_t phase = 0;
+      int stage = 0, it = 0, tail_stage = 0;
+      uint32_t phase = 0, tail_phase = 0;
       bool ok = true;
-      while (ok && uniform(walk.next(p, s_rows, s_pre))) {
+      const auto advance = [&] {
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      };
+      while (ok && uniform(walk.next(p, s_off, s_pre))) {
         const int nk = uniform(walk.t.nk), nr = uniform(walk.t.nr), cnt = uniform(walk.t.cnt);
         if (nk == 0) continue;
+        const int place = M == kWgrad ? tail_place<Tr>(nk, cnt) : nk;
         const uint32_t idesc = make_idesc_16(128 * CG, (nr + 15) & ~15, p.fmt, Tr::kAMN, Tr::kBMN);
         const int last = (cnt - (nk - 1) * kBK + 15) / 16;  // weight gradient: steps with rows
         for (int seg = 0; seg < nk && ok; seg += Tr::kSegment) {
@@ -470,13 +496,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t d = tmem_base + uint32_t(ab * NB);
           for (int kb0 = seg; kb0 < end; kb0 += KPS) {
             // a group's last k-block: the pair's warps 2 and 3 may have written to it
-            const bool is_tail = M == kWgrad && kb0 + 1 == nk && (cnt & 15) != 0;
-            ok = uniform(CG == 2 && is_tail ? mbar_wait_acquire_cluster(&full[stage], phase, abort)
-                                            : mbar_wait(&full[stage], phase, abort));
+            const bool is_tail = M == kWgrad && place < nk && kb0 + 1 == nk;
+            if (M == kWgrad && kb0 == place) {  // its stage; its turn comes last
+              tail_stage = stage;
+              tail_phase = phase;
+              advance();
+            }
+            const int at = is_tail ? tail_stage : stage;
+            ok = uniform(CG == 2 && is_tail
+                             ? mbar_wait_acquire_cluster(&full[at], tail_phase, abort)
+                             : mbar_wait(&full[at], is_tail ? tail_phase : phase, abort));
             if (!ok) break;
             tc_fence_after();
             const int kbn = min(KPS, nk - kb0);
-            const uint32_t sa0 = tiles_u32 + stage * Tr::kStageBytes;
+            const uint32_t sa0 = tiles_u32 + at * Tr::kStageBytes;
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < KPS; ++kk) {
@@ -494,13 +527,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     bd + s * (Tr::kBMN ? 128 : 2), idesc,
                                     (kb0 - seg) | kk | s ? 1u : 0u);
               }
-              umma_commit_cg<CG>(&empty[stage]);
+              umma_commit_cg<CG>(&empty[at]);
             }
             __syncwarp();
-            if (++stage == STAGES) {
-              stage = 0;
-              phase ^= 1u;
-            }
+            if (!is_tail) advance();
           }
           if (ok && elect_one()) umma_commit_cg<CG>(&tfull[ab]);
           __syncwarp();
@@ -523,12 +553,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int total = 0, tails = 0;
     uint32_t used = 0;  // phase bit of each of this warp's barriers
     uint64_t* mine = tail + (warp - 2) * STAGES;
-    while (walk.next(p, s_rows, s_pre)) {
+    while (walk.next(p, s_off, s_pre)) {
       const GTile& t = walk.t;
+      const int place = tail_place<Tr>(t.nk, t.cnt);
+      const int stage = (total + place) % STAGES;
       total += t.nk;
-      if ((t.cnt & 15) == 0) continue;  // whole steps of 16 rows
+      if (place == t.nk) continue;
       if ((tails++ & 1) != warp - 2) continue;
-      const int stage = (total - 1) % STAGES;
       if (!mbar_wait(&mine[stage], (used >> stage) & 1u, abort)) {
         give_up(p, abort);
         break;
@@ -557,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t st = smem_u32(staging) + (warp - 4) * Tr::kWarpStaging;
     int it = 0;
     bool ok = true;
-    while (ok && uniform(walk.next(p, s_rows, s_pre))) {
+    while (ok && uniform(walk.next(p, s_off, s_pre))) {
       const int nk = uniform(walk.t.nk), nr = uniform(walk.t.nr), r0 = uniform(walk.t.r0);
       const int e = uniform(walk.t.e);
       const int cw = uniform(walk.t.c0) + int(rank) * 128 + q * 32;
@@ -796,10 +827,10 @@ moe_status dispatch(GroupedArgs& a, const Operand& A, const Operand& B, bool out
     // 376 x 872: 7.1 for 9.2).
     const bool few = tiles(2, 256) < sms / 2;
     if (out_f32)
-      return few ? run_variant<M, 1, 128, 1, 5, 4>(a, A, B, dev, sms, stream)
-                 : run_variant<M, 2, 256, 1, 5, 4>(a, A, B, dev, sms, stream);
-    return few ? run_variant<M, 1, 128, 1, 5, 2>(a, A, B, dev, sms, stream)
-               : run_variant<M, 2, 256, 1, 5, 2>(a, A, B, dev, sms, stream);
+      return few ? run_variant<M, 1, 128, 1, 6, 4>(a, A, B, dev, sms, stream)
+                 : run_variant<M, 2, 256, 1, 6, 4>(a, A, B, dev, sms, stream);
+    return few ? run_variant<M, 1, 128, 1, 6, 2>(a, A, B, dev, sms, stream)
+               : run_variant<M, 2, 256, 1, 6, 2>(a, A, B, dev, sms, stream);
   }
 }
 

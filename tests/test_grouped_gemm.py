@@ -241,6 +241,15 @@ def test_tails_of_neighbouring_tiles_in_one_stage(blocks, f32):
     run("wgrad", [64 * blocks - 3] * 24, K=768, N=1536, dtype="bf16", f32=f32, seed=blocks)
 
 
+@pytest.mark.parametrize("f32", (False, True))
+@pytest.mark.parametrize("K,N", ((264, 520), (72, 56)))
+def test_tails_out_of_turn(f32, K, N):
+    # groups whose rows end inside a k-block, of one k-block and of more, around the borders of
+    # the 768-row pieces of an FP32 sum
+    run("wgrad", [1, 65, 767, 769, 129, 785, 833, 193, 897, 1537, 0, 1600, 63], K, N, "bf16",
+        f32=f32, tail=9)
+
+
 @pytest.mark.parametrize("bad", (float("inf"), float("nan")))
 @pytest.mark.parametrize("counts", ([10, 7, 3, 50], [400, 13, 77, 110]), ids=("few", "many"))
 def test_nonfinite_values_stay_in_their_group(counts, bad):
