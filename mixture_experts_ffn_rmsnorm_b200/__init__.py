@@ -143,8 +143,9 @@ def _need_torch():
     if _torch is None:
         import torch
         _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
-        _current_device = torch.cuda.current_device
-        # the current stream's handle without a Stream object (3 us less a call)
+        # the current device and stream without torch.cuda's wrappers (0.5 us less a call) and
+        # without a Stream object (3 us)
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda dev: torch.cuda.current_stream(dev).cuda_stream)
         _torch = torch
@@ -174,19 +175,19 @@ def _launch_stream(what, stream, *tensors) -> Optional[int]:
     return stream.cuda_stream or None
 
 
-def _rows_ld(t, what, name) -> int:
-    """Leading dimension of a row tensor [rows, width] (unit stride along a row)."""
+def _rows_of(t, what, name):
+    """Rows, width and leading dimension of a row tensor [rows, width] (unit stride along a row)."""
     st = t.stride()
     if len(st) != 2:
         raise MoEError(1, f"{what}: {name} is not two-dimensional")
     rows, width = t.shape
     if st[1] != 1 and width > 1 and rows > 0:
         raise MoEError(1, f"{what}: {name}'s rows are not contiguous")
-    return st[0] if rows > 1 else (width + 7) // 8 * 8
+    return rows, width, st[0] if rows > 1 else (width + 7) // 8 * 8
 
 
-def _experts_ld(t, what, name) -> int:
-    """Leading dimension of stacked matrices [E, N, K]: matrices back to back."""
+def _experts_of(t, what, name):
+    """Sizes and leading dimension of stacked matrices [E, N, K]: matrices back to back."""
     st = t.stride()
     if len(st) != 3:
         raise MoEError(1, f"{what}: {name} is not three-dimensional")
@@ -196,12 +197,13 @@ def _experts_ld(t, what, name) -> int:
     if N > 1:
         if E > 1 and st[0] != N * st[1]:
             raise MoEError(1, f"{what}: {name}'s matrices do not lie back to back")
-        return st[1]
-    return st[0] if E > 1 else (K + 7) // 8 * 8
+        return E, N, K, st[1]
+    return E, N, K, st[0] if E > 1 else (K + 7) // 8 * 8
 
 
 def _check_off(off, E, what):
-    if off.dtype != _torch.int32 or off.shape != (E + 1,) or not off.is_contiguous():
+    if off.dtype != _torch.int32 or off.dim() != 1 or off.numel() != E + 1 or (
+            not off.is_contiguous()):
         raise MoEError(1, f"{what}: off is not a contiguous int32 tensor [num_experts + 1]")
 
 
@@ -220,10 +222,10 @@ def grouped_gemm(x, w, off, y, relu2=False, status=None, stream=None):
     max(v, 0)^2.  status: optional int32 word the device ORs error bits into."""
     what = "moe_grouped_gemm"
     _torch or _need_torch()
-    ldx, ldw, ldy = _rows_ld(x, what, "x"), _experts_ld(w, what, "w"), _rows_ld(y, what, "y")
-    E, N, K = w.shape
-    rows = x.shape[0]
-    if x.shape[1] != K or y.shape != (rows, N):
+    E, N, K, ldw = _experts_of(w, what, "w")
+    rows, in_x, ldx = _rows_of(x, what, "x")
+    rows_y, out_y, ldy = _rows_of(y, what, "y")
+    if in_x != K or out_y != N or rows_y != rows:
         raise MoEError(1, f"{what}: shapes {tuple(x.shape)}, {tuple(w.shape)}, {tuple(y.shape)}")
     dt = _dtype_code(x, what)
     if w.dtype != x.dtype or y.dtype != x.dtype:
@@ -245,10 +247,10 @@ def grouped_gemm_dgrad(dy, w, off, dx, status=None, stream=None):
     dy [rows, N], w [E, N, K], dx [rows, K]; the rest as in grouped_gemm."""
     what = "moe_grouped_gemm_dgrad"
     _torch or _need_torch()
-    ldy, ldw, ldx = _rows_ld(dy, what, "dy"), _experts_ld(w, what, "w"), _rows_ld(dx, what, "dx")
-    E, N, K = w.shape
-    rows = dy.shape[0]
-    if dy.shape[1] != N or dx.shape != (rows, K):
+    E, N, K, ldw = _experts_of(w, what, "w")
+    rows, out_y, ldy = _rows_of(dy, what, "dy")
+    rows_x, in_x, ldx = _rows_of(dx, what, "dx")
+    if in_x != K or out_y != N or rows_x != rows:
         raise MoEError(1, f"{what}: shapes {tuple(dy.shape)}, {tuple(w.shape)}, {tuple(dx.shape)}")
     dt = _dtype_code(dy, what)
     if w.dtype != dy.dtype or dx.dtype != dy.dtype:
@@ -272,10 +274,10 @@ def grouped_gemm_wgrad(dy, x, off, dw, accumulate=False, status=None, stream=Non
     accumulate (float32 only) adds to dw.  The rest as in grouped_gemm."""
     what = "moe_grouped_gemm_wgrad"
     _torch or _need_torch()
-    ldy, ldx, ldw = _rows_ld(dy, what, "dy"), _rows_ld(x, what, "x"), _experts_ld(dw, what, "dw")
-    E, N, K = dw.shape
-    rows = dy.shape[0]
-    if dy.shape[1] != N or x.shape != (rows, K):
+    E, N, K, ldw = _experts_of(dw, what, "dw")
+    rows, out_y, ldy = _rows_of(dy, what, "dy")
+    rows_x, in_x, ldx = _rows_of(x, what, "x")
+    if in_x != K or out_y != N or rows_x != rows:
         raise MoEError(1, f"{what}: shapes {tuple(dy.shape)}, {tuple(x.shape)}, {tuple(dw.shape)}")
     dt, odt = _dtype_code(dy, what), _dtype_code(dw, what)
     if x.dtype != dy.dtype:
@@ -313,15 +315,18 @@ def nvfp4_gemv(x, idx, w, w_scale, w_scale2, y, relu2=False, status=None, stream
             w_scale2.dtype != torch.float32):
         raise MoEError(1, f"{what}: dtypes {w.dtype}, {w_scale.dtype}, {w_scale2.dtype}")
     per_slot = x.dim() == 3
-    if x.shape != ((T, k, K) if per_slot else (T, K)) or y.shape != (T, k, N) or (
+    if per_slot:
+        rows, slots, in_x, ldx = _experts_of(x, what, "x")
+    else:
+        (rows, in_x, ldx), slots = _rows_of(x, what, "x"), k
+    rows_y, slots_y, out_y, ldy = _experts_of(y, what, "y")
+    if (rows, slots, in_x, rows_y, slots_y, out_y) != (T, k, K, T, k, N) or (
             w_scale.shape != (E, N, K // 16) or w_scale2.numel() != E):
         raise MoEError(1, f"{what}: shapes {tuple(x.shape)}, {tuple(idx.shape)}, {tuple(w.shape)}, "
                           f"{tuple(w_scale.shape)}, {tuple(w_scale2.shape)}, {tuple(y.shape)}")
     dt = _dtype_code(x, what)
     if y.dtype != x.dtype:
         raise MoEError(1, f"{what}: x and y have different dtypes")
-    ldx = _experts_ld(x, what, "x") if per_slot else _rows_ld(x, what, "x")
-    ldy = _experts_ld(y, what, "y")
     _check_status(status, what)
     s = _launch_stream(what, stream, x, idx, w, w_scale, w_scale2, y, status)
     st = (_lib or load_library()).moe_nvfp4_gemv(
