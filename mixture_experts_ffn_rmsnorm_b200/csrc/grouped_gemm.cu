@@ -24,7 +24,7 @@
 // shared between calls).
 //   warp 0    issues the TMA loads into a ring of stages;
 //   warp 1    (of the pair's rank 0) issues the tcgen05.mma;
-//   warps 2, 3 weight gradient: zero the rows of a group's last k-block that
+//   warp 2    weight gradient: zeroes the rows of a group's last k-block that
 //             belong to the next group, in shared memory;
 //   warps 4-11 read the accumulators from TMEM and store them, while the MMA
 //             warp fills the other accumulator.
@@ -58,7 +58,9 @@ constexpr int kBK = 64;        // elements of q per k-block (128 bytes)
 
 struct GroupedArgs {
   CUtensorMap tmA;     // forward: 128-row boxes; else 64-row boxes
-  CUtensorMap tmB[4];  // K-major: boxes of 16, 32, 64 and 128 rows; weight gradient: [0], 64
+  // K-major: boxes of 16, 32, 64 and 128 rows; weight gradient: [0] of 64, [1]
+  // and [2] of 1 and 4, for zeros
+  CUtensorMap tmB[4];
   CUtensorMap tmO;     // weight gradient with `tma_out`: a round's 32 or 64 r's x 32 c's of the output
   const int* off;
   int groups;
@@ -99,14 +101,14 @@ struct Traits {
   static constexpr int kSegment = EB == 4 ? 12 : 1 << 30;  // k-blocks
   // Weight gradient: a group's last k-block is loaded this many k-blocks ahead of
   // its turn, in which time the rows behind the group's last one are cleared
-  // (128 groups of 500 / 333 / 261 / 135 rows, 2688 x 1856, us: 0 ahead 805 / 573
-  // / 511 / 361, 2 ahead 773 / 565 / 495 / 365; with five stages instead of six
-  // 0 ahead 807 / 624 / 520 / 380, 3 ahead 784 / 619 / 550 / 380).
-  static constexpr int kAhead = 2;
+  // (128 groups of 500 / 333 / 261 / 135 rows, 2688 x 1856, us: 0 ahead 725 / 553
+  // / 497 / 346, 1 ahead 688 / 533 / 492 / 340, 2 ahead 709 / 538 / 481 / 351, 3
+  // ahead 741 / 572 / 493 / 346).
+  static constexpr int kAhead = 1;
   static_assert(M != kWgrad || kAhead < STAGES, "");
   // behind the stages and the staging tiles: barriers, the groups' bounds, row
   // tiles before each group, a scan's sums
-  static constexpr int kBarriers = (4 * STAGES + 6) * 8;
+  static constexpr int kBarriers = (3 * STAGES + 6) * 8;
   static constexpr int kSmem = STAGES * kStageBytes + kStagingBytes + kBarriers +
                                (2 * (MOE_MAX_EXPERTS + 1) + kThreads / 32) * 4;
   static_assert(!kBMN || KPS == 1, "the tail of a group is one k-block of one stage");
@@ -311,13 +313,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* staging = tiles + STAGES * Tr::kStageBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + Tr::kStagingBytes);
   uint64_t* empty = full + STAGES;
-  uint64_t* tail = empty + STAGES;  // two sets, one for each of the warps 2 and 3
-  uint64_t* tfull = tail + 2 * STAGES;
+  uint64_t* tail = empty + STAGES;
+  uint64_t* tfull = tail + STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(Tr::kBarriers == (4 * STAGES + 5) * 8 + 8, "");
+  static_assert(Tr::kBarriers == (3 * STAGES + 5) * 8 + 8, "");
   int* s_off = reinterpret_cast<int*>(full) + Tr::kBarriers / 4;  // groups' bounds
   int* s_pre = s_off + MOE_MAX_EXPERTS + 1;
   int* s_scan = s_pre + MOE_MAX_EXPERTS + 1;
@@ -331,7 +333,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[s], CG);
       mbar_init(&empty[s], 1);
       mbar_init(&tail[s], 1);
-      mbar_init(&tail[STAGES + s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    int stage = 0, tails = 0;
+    int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
     while (ok && uniform(walk.next(p, s_off, s_pre))) {
@@ -419,9 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
           uint32_t bar;
           if (is_tail) {
-            uint64_t* tb = &tail[(tails & 1) * STAGES + stage];
-            mbar_arrive_expect_tx(tb, bytes);
-            bar = smem_u32(tb);
+            mbar_arrive_expect_tx(&tail[stage], bytes);
+            bar = smem_u32(&tail[stage]);
           } else if (CG == 2) {
             bar = map_to_rank(smem_u32(&full[stage]), 0);
             mbar_arrive_expect_tx_at(bar, bytes);
@@ -451,7 +451,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
-        tails += is_tail;
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;
@@ -495,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t d = tmem_base + uint32_t(ab * NB);
           for (int kb0 = seg; kb0 < end; kb0 += KPS) {
-            // a group's last k-block: the pair's warps 2 and 3 may have written to it
+            // a group's last k-block with rows to clear
             const bool is_tail = M == kWgrad && place < nk && kb0 + 1 == nk;
             if (M == kWgrad && kb0 == place) {  // its stage; its turn comes last
               tail_stage = stage;
@@ -503,9 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               advance();
             }
             const int at = is_tail ? tail_stage : stage;
-            ok = uniform(CG == 2 && is_tail
-                             ? mbar_wait_acquire_cluster(&full[at], tail_phase, abort)
-                             : mbar_wait(&full[at], is_tail ? tail_phase : phase, abort));
+            ok = uniform(mbar_wait(&full[at], is_tail ? tail_phase : phase, abort));
             if (!ok) break;
             tc_fence_after();
             const int kbn = min(KPS, nk - kb0);
@@ -543,43 +540,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       int zero = 0;
       mbar_wait(drain, 0, &zero);
     }
-  } else if (M == kWgrad && (warp == 2 || warp == 3)) {
+  } else if (M == kWgrad && warp == 2) {
     // ---------------------------------------- rows behind a group's last one
-    // Two warps take turns: clearing, the fences and the hand-over to the
-    // pair's other CTA take about a microsecond, a tile of one k-block 0.5.
-    // Each has barriers of its own: neighbouring tails may share a stage, and
-    // a barrier that completes a phase for the other warp in between would
-    // answer this one's wait too early.
-    int total = 0, tails = 0;
-    uint32_t used = 0;  // phase bit of each of this warp's barriers
-    uint64_t* mine = tail + (warp - 2) * STAGES;
-    while (walk.next(p, s_off, s_pre)) {
-      const GTile& t = walk.t;
-      const int place = tail_place<Tr>(t.nk, t.cnt);
+    // Cleared by copies of boxes that lie behind the tensor's last row, which
+    // TMA fills with zeros: they complete on the MMA's barrier like the loads
+    // before them.  (Plain stores have to be released to the pair's other CTA,
+    // about a microsecond a tail: 48 rows a group 259 us, this 245; 500 rows
+    // 773 and 680.)
+    int total = 0;
+    uint32_t used = 0;  // phase bit of each barrier
+    while (uniform(walk.next(p, s_off, s_pre))) {
+      const int nk = uniform(walk.t.nk), cnt = uniform(walk.t.cnt);
+      const int place = tail_place<Tr>(nk, cnt);
       const int stage = (total + place) % STAGES;
-      total += t.nk;
-      if (place == t.nk) continue;
-      if ((tails++ & 1) != warp - 2) continue;
-      if (!mbar_wait(&mine[stage], (used >> stage) & 1u, abort)) {
-        give_up(p, abort);
+      total += nk;
+      if (place == nk) continue;
+      if (!uniform(mbar_wait(&tail[stage], (used >> stage) & 1u, abort))) {
+        if (lane == 0) give_up(p, abort);
         break;
       }
       used ^= 1u << stage;
-      const int nb = ((t.nr + 15) & ~15) / CG;
+      const int nb = ((uniform(walk.t.nr) + 15) & ~15) / CG;
       const int blocks = 2 + (nb + 63) / 64;
-      const int valid = t.cnt & (kBK - 1), end = (valid + 15) & ~15;
-      for (int h = 0; h < blocks; ++h) {
-        uint32_t* blk = reinterpret_cast<uint32_t*>(tiles + stage * Tr::kStageBytes + h * 8192);
-        for (int r = valid; r < end; ++r) blk[r * 32 + lane] = 0u;  // whole rows: swizzled or not
+      const int valid = cnt & (kBK - 1), n = -valid & 15;  // rows to clear
+      if (elect_one()) {
+        uint32_t bar = smem_u32(&full[stage]);
+        if (CG == 2) {
+          bar = map_to_rank(bar, 0);
+          mbar_arrive_expect_tx_at(bar, uint32_t(blocks * n) * 128);
+        } else {
+          mbar_arrive_expect_tx(&full[stage], uint32_t(blocks * n) * 128);
+        }
+        for (int h = 0; h < blocks; ++h) {
+          uint32_t dst = tiles_u32 + stage * Tr::kStageBytes + h * 8192 + valid * 128;
+          for (int r = 0; r < n;) {
+            const int size = n - r >= 4 ? 2 : 1;
+            tma_load_3d<CG>(dst, &p.tmB[size], bar, 0, p.rows, 0);
+            r += size == 2 ? 4 : 1;
+            dst += size == 2 ? 512 : 128;
+          }
+        }
       }
-      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        if (CG == 2 && rank != 0)
-          mbar_arrive_release_at(map_to_rank(smem_u32(&full[stage]), 0));
-        else
-          mbar_arrive(&full[stage]);
-      }
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
@@ -743,11 +745,11 @@ struct Operand {
   int inner, rows, groups;
 };
 
-bool map_of(CUtensorMap* m, const Operand& o, uint32_t fmt, int box_rows) {
+bool map_of(CUtensorMap* m, const Operand& o, uint32_t fmt, int box_rows, bool swizzle = true) {
   return make_map_3d(m, fmt ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
                      o.base, uint64_t(o.inner), uint64_t(o.rows), uint64_t(o.groups),
                      uint64_t(o.ld) * 2, uint64_t(o.ld) * 2 * uint64_t(o.groups > 1 ? o.rows : 1),
-                     uint32_t(box_rows));
+                     uint32_t(box_rows), 128, swizzle);
 }
 
 template <Mode M, int CG, int NB, int KPS, int STAGES, int EB>
@@ -756,7 +758,9 @@ moe_status run_variant(GroupedArgs& a, const Operand& A, const Operand& B, int d
   using V = Variant<M, CG, NB, KPS, STAGES, EB>;
   bool ok = map_of(&a.tmA, A, a.fmt, M == kFwd ? 128 : 64);
   if (M == kWgrad)
-    ok = ok && map_of(&a.tmB[0], B, a.fmt, 64);
+    // and boxes of zeros: 1 and 4 rows
+    ok = ok && map_of(&a.tmB[0], B, a.fmt, 64) && map_of(&a.tmB[1], A, a.fmt, 1, false) &&
+         map_of(&a.tmB[2], A, a.fmt, 4, false);
   else
     for (int i = 0; i < 4 && (16 << i) <= NB / CG; ++i)
       ok = ok && map_of(&a.tmB[i], B, a.fmt, 16 << i);

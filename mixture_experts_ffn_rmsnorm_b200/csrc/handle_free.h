@@ -78,14 +78,14 @@ inline bool encode_bound(const F& encode) {
   return r == CUDA_SUCCESS;
 }
 
-// 3-D map of a row-major tensor [groups, rows, inner]: box = one swizzle span
-// (128 bytes, or 64) of the inner extent x box_rows rows of one group; loads
-// zero-fill beyond each extent, stores leave it out.  Strides in bytes,
-// multiples of 16.
+// 3-D map of a row-major tensor [groups, rows, inner]: box = one span (128
+// bytes, or 64) of the inner extent x box_rows rows of one group, swizzled over
+// the span or not; loads zero-fill beyond each extent, stores leave it out.
+// Strides in bytes, multiples of 16.
 inline bool make_map_3d(CUtensorMap* m, CUtensorMapDataType type, uint32_t elem_bytes,
                         const void* base, uint64_t inner, uint64_t rows, uint64_t groups,
                         uint64_t row_stride, uint64_t group_stride, uint32_t box_rows,
-                        uint32_t span = 128) {
+                        uint32_t span = 128, bool swizzle = true) {
   const EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
   const cuuint64_t dims[3] = {inner, rows, groups};
@@ -95,7 +95,9 @@ inline bool make_map_3d(CUtensorMap* m, CUtensorMapDataType type, uint32_t elem_
   return encode_bound([&] {
     return enc(m, type, 3, const_cast<void*>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE,
-               span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               !swizzle      ? CU_TENSOR_MAP_SWIZZLE_NONE
+               : span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                             : CU_TENSOR_MAP_SWIZZLE_64B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   });
 }

@@ -53,34 +53,10 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// The same, publishing this thread's earlier shared-memory writes.
-__device__ __forceinline__ void mbar_arrive_release_at(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
-
 __device__ __forceinline__ void mbar_arrive_expect_tx_at(uint32_t cluster_addr, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
                "r"(bytes)
                : "memory");
-}
-
-// mbar_wait of ptx.cuh that also acquires what other CTAs of the cluster
-// released on the barrier (mbar_arrive_release_at).
-__device__ __forceinline__ bool mbar_wait_acquire_cluster(uint64_t* bar, uint32_t parity,
-                                                          volatile int* abort) {
-  if (!mbar_wait(bar, parity, abort)) return false;
-  // the phase is complete: this returns at once (a fence.acq_rel.cluster in
-  // its place took 0.4 us)
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 
 // 3-D tiled load of one box into this CTA's shared memory.  CG = 2: the
