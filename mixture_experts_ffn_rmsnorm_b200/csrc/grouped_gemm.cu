@@ -37,9 +37,10 @@
 // 128 experts): few rows a group, the weights' stream: 8 tokens 64 us, 48 rows
 // a group 204 us (6.4 and 6.5 TB/s); many, the tensor cores under the 1000 W
 // cap: dense 8192 x 4096 x 4096 194 us (1417 TFLOP/s; in a burst 172 us), 384
-// rows a group on average but 7300 on the hottest 530 us (920).  Weight
-// gradients of few rows, the writes: 48 rows a group 261 us (5.1 TB/s; plain
-// stores of zeros to the same 1.28 GB take 320), 256 rows in FP32 345 us (4.8).
+// rows a group on average but 7300 on the hottest 500 to 530 us (970 to 920).
+// Weight gradients of few rows, the writes: 48 rows a group 247 us (5.4 TB/s;
+// plain stores of zeros to the same 1.28 GB take 320), 256 rows in FP32 325 us
+// (5.1).
 #include <cuda_fp16.h>
 
 #include "handle_free.h"
