@@ -939,8 +939,10 @@ extern "C" moe_status moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const
   a.fmt = dtype == MOE_DTYPE_BF16;
   a.accumulate = accumulate;
   a.vec = !f32 && aligned_to(dw, 16) && (lddw & 7) == 0;
-  // a group's stride below TMA's 2^40 bytes too
-  a.tma_out = !accumulate && aligned_to(dw, 16) && (lddw * (f32 ? 4 : 2)) % 16 == 0 &&
+  // whole 16-byte blocks, or a store would write to the end of a row's last one,
+  // and a group's stride below TMA's 2^40 bytes
+  const int block = f32 ? 4 : 8;
+  a.tma_out = !accumulate && aligned_to(dw, 16) && in_features % block == 0 && lddw % block == 0 &&
               a.group_stride < (1LL << 37);
   a.status = status;
   // no rows: every group is empty and no map is read through; the maps still

@@ -190,6 +190,35 @@ def test_strides_and_rows_outside_the_groups(mode, counts):
     run(mode, counts, K=200, N=136, dtype="bf16", start=1, tail=1, pad=3)
 
 
+@pytest.mark.parametrize("mode", MODES + ("wgrad_f32",))
+@pytest.mark.parametrize("counts", ([3, 0, 40, 1], [300, 0, 70, 513]), ids=("few", "many"))
+@pytest.mark.parametrize("width,lead,at", ((130, 140, 1), (257, 260, 2), (261, 261, 0), (64, 67, 3),
+                                           (384, 388, 4), (128, 129, 1), (95, 104, 7), (33, 40, 8),
+                                           (250, 256, 0), (36, 40, 8)))
+def test_outputs_off_16_byte_boundaries(mode, counts, width, lead, at):
+    # rows `lead` elements apart that begin `at` elements into the tensor; what lies beside them stays
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    mode, f32 = mode[:5], mode.endswith("f32")
+    K, N = (72, width) if mode == "fwd" else (width, 72)
+    E, rows, off = len(counts), sum(counts), offsets(counts)
+    x, dy = padded((rows, K), torch.bfloat16, gen), padded((rows, N), torch.bfloat16, gen)
+    w = padded((E, N, K), torch.bfloat16, gen)
+    shape = (E, N) if mode == "wgrad" else (rows,)
+    store = torch.full((int(np.prod(shape)) * lead + 16,), 7.0, device="cuda",
+                       dtype=torch.float32 if f32 else torch.bfloat16)
+    out = store[at:at + int(np.prod(shape)) * lead].view(*shape, lead)[..., :width]
+    if mode == "fwd":
+        moe.grouped_gemm(x, w, off, out)
+    elif mode == "dgrad":
+        moe.grouped_gemm_dgrad(dy, w, off, out)
+    else:
+        moe.grouped_gemm_wgrad(dy, x, off, out)
+    ref, mag = reference(mode, off, E, dy, x, w)
+    check(out, *bound(ref, mag, 513 if mode == "wgrad" else 72, out.dtype), (mode, width))
+    out.fill_(7.0)
+    assert (store == 7.0).all()
+
+
 @pytest.mark.parametrize("counts", ([10, 0, 3, 50], [400, 0, 77, 1100]), ids=("few", "many"))
 def test_fused_relu2(counts):
     run("fwd", counts, K=264, N=192, dtype="bf16", relu2=True)
