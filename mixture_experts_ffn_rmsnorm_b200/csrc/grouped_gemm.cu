@@ -610,10 +610,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t tb = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(ab * NB);
         const bool mine = cw < p.C;  // the warp has c's to store
+        const bool bulk = M == kWgrad && p.tma_out;
+        const bool add = EB == 4 && (p.accumulate || seg > 0);
+        if (EB == 4 && bulk && seg > 0) {  // the sums before are in memory
+          if (elect_one()) bulk_wait_all();
+          __syncwarp();
+        }
 #pragma unroll 1
         for (int j0 = half * 32 * Tr::kRound; j0 < nr && mine; j0 += 64 * Tr::kRound) {
           // the bulk store of the round before has read the staging tile
-          const bool bulk = M == kWgrad && p.tma_out && nk <= Tr::kSegment;
           if (bulk) {
             if (elect_one()) bulk_wait_read<0>();
             __syncwarp();
@@ -631,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               stage_chunk_32(r, st);
             else if (cw + lane < p.C)
               store_chunk_32(p, r, static_cast<float*>(p.out) + base + j0 * p.ldo + cw + lane,
-                             nr - j0, p.accumulate || seg > 0);
+                             nr - j0, add);
           } else {
             uint32_t r[2 * Tr::kRound][16];
             if (nk > 0) {
@@ -664,7 +669,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (elect_one()) {
-              tma_store_3d(&p.tmO, st, cw, r0 + j0, e);
+              if (add)
+                tma_add_3d(&p.tmO, st, cw, r0 + j0, e);
+              else
+                tma_store_3d(&p.tmO, st, cw, r0 + j0, e);
               bulk_commit();
             }
           }
@@ -942,7 +950,7 @@ extern "C" moe_status moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const
   // whole 16-byte blocks, or a store would write to the end of a row's last one,
   // and a group's stride below TMA's 2^40 bytes
   const int block = f32 ? 4 : 8;
-  a.tma_out = !accumulate && aligned_to(dw, 16) && in_features % block == 0 && lddw % block == 0 &&
+  a.tma_out = aligned_to(dw, 16) && in_features % block == 0 && lddw % block == 0 &&
               a.group_stride < (1LL << 37);
   a.status = status;
   // no rows: every group is empty and no map is read through; the maps still

@@ -246,6 +246,41 @@ def accumulated(counts, K, N):
     assert torch.equal(dw[1], before[1])  # nothing to add to an empty group
 
 
+@pytest.mark.parametrize("K", (64, 65))
+def test_accumulation_onto_small_and_special_values(K):
+    # subnormals, infinities and NaN in the gradient that is added to; a sum of nothing but zeros
+    E, N, counts = 3, 40, [900, 5, 0]
+    rows, off = sum(counts), offsets(counts)
+    x = torch.zeros(rows, (K + 7) // 8 * 8, dtype=torch.bfloat16, device="cuda")[:, :K]
+    dy = torch.ones(rows, N, dtype=torch.bfloat16, device="cuda")
+    x[900] = 1.0  # group 1: every sum is 1
+    row = torch.tensor([1e-40, -3e-42, float("inf"), -float("inf"), float("nan"), 2.0, -0.5, 1e30])
+    dw = row.cuda().repeat(E * N * K // 8 + 1)[:E * N * K].view(E, N, K).clone()
+    before = dw.clone()
+    moe.grouped_gemm_wgrad(dy, x, off, dw, accumulate=True)
+    torch.testing.assert_close(dw[0], before[0], rtol=0, atol=0, equal_nan=True)
+    torch.testing.assert_close(dw[1], before[1] + 1.0, rtol=0, atol=0, equal_nan=True)
+    torch.testing.assert_close(dw[2], before[2], rtol=0, atol=0, equal_nan=True)
+
+
+@pytest.mark.parametrize("f32_counts", ([900, 65, 1537, 0, 2000], [769] * 6))
+def test_accumulation_is_deterministic(f32_counts):
+    gen = torch.Generator(device="cuda").manual_seed(41)
+    K, N, E, rows, off = 264, 520, len(f32_counts), sum(f32_counts), offsets(f32_counts)
+    x, dy = padded((rows, K), torch.bfloat16, gen), padded((rows, N), torch.bfloat16, gen)
+    start = torch.randn(E, N, K, device="cuda", generator=gen)
+    runs = []
+    for _ in range(4):
+        dw = start.clone()
+        moe.grouped_gemm_wgrad(dy, x, off, dw, accumulate=True)
+        moe.grouped_gemm_wgrad(dy, x, off, dw, accumulate=True)
+        runs.append(dw)
+    assert all(torch.equal(runs[0], r) for r in runs[1:])
+    ref, mag = reference("wgrad", off, E, dy, x, None)
+    q = 2 * max(f32_counts) + 1
+    check(runs[0], *bound(start.double() + 2 * ref, start.double().abs() + 2 * mag, q, dw.dtype), "acc")
+
+
 @pytest.mark.parametrize("rows,K,N", ((8192, 512, 512), (8191, 2048, 2304), (769, 96, 40)))
 def test_long_sums_in_32_bits(rows, K, N):
     # Every addition of a k-step truncates by less than an ulp (2^-23) of the partial sum.  Sums of
