@@ -97,9 +97,11 @@ struct Traits {
   static constexpr int kStagingBytes = kEpiWarps * kWarpStaging;
   // The tensor cores truncate as they accumulate: a sum of n rows loses about
   // n * 1e-9 of itself (measured: 9e-6 at 8192).  A 16-bit result hides that;
-  // for an FP32 one the sums start anew every 768 rows (7e-7) and are added up
-  // by the epilogue, rounding to nearest.
-  static constexpr int kSegment = EB == 4 ? 12 : 1 << 30;  // k-blocks
+  // for an FP32 one the sums start anew every 768 rows (7e-7) and are added up,
+  // rounding to nearest: two in the epilogue, which takes both accumulators
+  // then, and every two sums in memory.  (128 groups of 780 rows, 1024 x 2688:
+  // 819 us with each added up in memory, 694 with pairs.)
+  static constexpr int kSegment = EB == 4 ? 12 : 1 << 28;  // k-blocks
   // Weight gradient: a group's last k-block is loaded this many k-blocks ahead of
   // its turn, in which time the rows behind the group's last one are cleared
   // (128 groups of 500 / 333 / 261 / 135 rows, 2688 x 1856, us: 0 ahead 725 / 553
@@ -597,15 +599,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cw = uniform(walk.t.c0) + int(rank) * 128 + q * 32;
       const long long row = M == kWgrad ? r0 : (long long)(uniform(walk.t.row0)) + r0;
       const long long base = (M == kWgrad ? e * p.group_stride : 0) + row * p.ldo;
-      for (int seg = 0; seg == 0 || (seg < nk && ok); seg += Tr::kSegment) {
+      for (int seg = 0; seg == 0 || (seg < nk && ok); seg += 2 * Tr::kSegment) {
         const int ab = it & 1;
+        const bool two = EB == 4 && nk - seg > Tr::kSegment;  // sums to join
         if (nk > 0) {
-          if (!uniform(mbar_wait(&tfull[ab], (it >> 1) & 1, abort))) {
+          ok = uniform(mbar_wait(&tfull[ab], (it >> 1) & 1, abort));
+          ++it;
+          if (two && ok) {
+            ok = uniform(mbar_wait(&tfull[ab ^ 1], (it >> 1) & 1, abort));
+            ++it;
+          }
+          if (!ok) {
             if (lane == 0) give_up(p, abort);
-            ok = false;
             break;
           }
-          ++it;
           tc_fence_after();
         }
         const uint32_t tb = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(ab * NB);
@@ -625,7 +632,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if constexpr (EB == 4) {
             uint32_t r[32];
-            if (nk > 0) {
+            if (two) {
+              const uint32_t tb2 = tmem_base + (uint32_t(q * 32) << 16) + uint32_t((ab ^ 1) * NB);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t s[2][16];
+                tmem_ld_32x32b_x16(tb + uint32_t(j0 + 16 * h), s[0]);
+                tmem_ld_32x32b_x16(tb2 + uint32_t(j0 + 16 * h), s[1]);
+                tmem_ld_wait_regs(s);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  r[16 * h + j] =
+                      __float_as_uint(__uint_as_float(s[0][j]) + __uint_as_float(s[1][j]));
+              }
+            } else if (nk > 0) {
               tmem_ld_32x32b_x32(tb + uint32_t(j0), r);
               tmem_ld_wait();
             } else {  // an empty group's gradient
@@ -680,14 +700,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (nk > 0) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
+          if (lane < 1 + two) {
             if (CG == 2)
-              mbar_arrive_at(map_to_rank(smem_u32(&tempty[ab]), 0));
+              mbar_arrive_at(map_to_rank(smem_u32(&tempty[ab ^ lane]), 0));
             else
-              mbar_arrive(&tempty[ab]);
+              mbar_arrive(&tempty[ab ^ lane]);
           }
         }
-        if (Tr::kSegment >= nk) break;
       }
     }
     if (M == kWgrad && elect_one()) bulk_wait_all();
