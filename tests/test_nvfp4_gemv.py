@@ -106,6 +106,61 @@ def test_widths(N, K):
     run(8, 1, E=1, N=N, K=K, dtype="fp16", seed=K + N)
 
 
+def test_widest_outputs():
+    run(3, 2, E=4, N=131072, K=32)
+
+
+@pytest.mark.parametrize("lead,at", ((70, 1), (67, 3), (64, 2)))
+def test_outputs_off_16_byte_boundaries(lead, at):
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    T, k, E, N, K = 3, 2, 5, 64, 96
+    w, s, s2 = weights(E, N, K, gen)
+    x = torch.randn(T, K, device="cuda", generator=gen).to(torch.bfloat16)
+    idx = torch.rand(T, E, device="cuda", generator=gen).topk(k, dim=1).indices.to(torch.int32)
+    store = torch.full((T * k * lead + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = store[at:at + T * k * lead].view(T, k, lead)[..., :N]
+    moe.nvfp4_gemv(x, idx, w, s, s2, y)
+    check(y, *expected(x, idx, w, s, s2, False, y.dtype))
+    y.fill_(7.0)
+    assert (store == 7.0).all()
+
+
+def test_beside_the_grouped_products_on_other_streams():
+    # four streams at once, every result the lone call's bit by bit
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    E, N, K, T, k = 12, 200, 256, 6, 4
+    w, s, s2 = weights(E, N, K, gen)
+    x = torch.randn(T, K, device="cuda", generator=gen).to(torch.bfloat16)
+    idx = torch.rand(T, E, device="cuda", generator=gen).topk(k, dim=1).indices.to(torch.int32)
+    rows = 900
+    off = torch.tensor([0, 10, 10, 300] + [500] * 8 + [rows], dtype=torch.int32, device="cuda")
+    xr = torch.randn(rows, K, device="cuda", generator=gen).to(torch.bfloat16)
+    dy = torch.randn(rows, N, device="cuda", generator=gen).to(torch.bfloat16)
+    wd = torch.randn(E, N, K, device="cuda", generator=gen).to(torch.bfloat16)
+
+    def outputs():
+        z = lambda *sh, dt=torch.bfloat16: torch.zeros(*sh, dtype=dt, device="cuda")  # noqa: E731
+        return [z(T, k, N), z(rows, N), z(rows, K), z(E, N, K, dt=torch.float32)]
+
+    calls = [lambda o, st: moe.nvfp4_gemv(x, idx, w, s, s2, o[0], stream=st),
+             lambda o, st: moe.grouped_gemm(xr, wd, off, o[1], stream=st),
+             lambda o, st: moe.grouped_gemm_dgrad(dy, wd, off, o[2], stream=st),
+             lambda o, st: moe.grouped_gemm_wgrad(dy, xr, off, o[3], accumulate=True, stream=st)]
+    alone = outputs()
+    for c in calls:
+        c(alone, None)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    many = [outputs() for _ in range(10)]
+    torch.cuda.synchronize()
+    for out in many:
+        for c, st in zip(calls, streams):
+            c(out, st)
+    torch.cuda.synchronize()
+    for out in many:
+        assert all(torch.equal(a, b) for a, b in zip(alone, out))
+
+
 def test_one_expert_for_all_rows():
     idx = torch.full((30, 2), 4, dtype=torch.int32, device="cuda")
     run(30, 2, E=5, N=40, K=256, idx=idx, per_slot=True)
