@@ -111,7 +111,7 @@ struct Traits {
   static_assert(M != kWgrad || kAhead < STAGES, "");
   // behind the stages and the staging tiles: barriers, the groups' bounds, row
   // tiles before each group, a scan's sums
-  static constexpr int kBarriers = (3 * STAGES + 6) * 8;
+  static constexpr int kBarriers = (3 * STAGES + 7) * 8;
   static constexpr int kSmem = STAGES * kStageBytes + kStagingBytes + kBarriers +
                                (2 * (MOE_MAX_EXPERTS + 1) + kThreads / 32) * 4;
   static_assert(!kBMN || KPS == 1, "the tail of a group is one k-block of one stage");
@@ -189,6 +189,24 @@ struct Walk {
 __device__ __forceinline__ void give_up(const GroupedArgs& p, volatile int* abort) {
   *abort = 1;
   if (p.status) atomicOr(p.status, kStatusWaitTimeout);
+}
+
+// mbar_wait for a warp whose turn may be many tiles away: the limit holds for
+// the time in which *begun, the count of tiles begun, stands still.
+__device__ __forceinline__ bool mbar_wait_turn(uint64_t* bar, uint32_t parity, volatile int* begun,
+                                               volatile int* abort) {
+  int seen = *begun;
+  long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort) return false;
+    const int now = *begun;
+    if (now != seen) {
+      seen = now;
+      t0 = clock64();
+    }
+    if (clock64() - t0 > kWaitLimitCycles) return false;
+  }
+  return true;
 }
 
 __device__ __forceinline__ float relu2(float v) {
@@ -322,7 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(Tr::kBarriers == (3 * STAGES + 5) * 8 + 8, "");
+  volatile int* begun = abort + 1;  // tiles the producer has begun
+  static_assert(Tr::kBarriers == (3 * STAGES + 5) * 8 + 16, "");
   int* s_off = reinterpret_cast<int*>(full) + Tr::kBarriers / 4;  // groups' bounds
   int* s_pre = s_off + MOE_MAX_EXPERTS + 1;
   int* s_scan = s_pre + MOE_MAX_EXPERTS + 1;
@@ -343,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(drain, 1);
     *abort = 0;
+    *begun = 0;
     fence_barrier_init();
     tma_prefetch_desc(&p.tmA);
     tma_prefetch_desc(&p.tmB[0]);
@@ -392,7 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    while (ok && uniform(walk.next(p, s_off, s_pre))) {
+    for (int it = 1; ok && uniform(walk.next(p, s_off, s_pre)); ++it) {
+      if (M == kWgrad && lane == 0) *begun = it;
       const int nk = uniform(walk.t.nk), nr = uniform(walk.t.nr), cnt = uniform(walk.t.cnt);
       const int e = uniform(walk.t.e), row0 = uniform(walk.t.row0), r0 = uniform(walk.t.r0);
       const int nmma = (nr + 15) & ~15;
@@ -550,6 +571,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // before them.  (Plain stores have to be released to the pair's other CTA,
     // about a microsecond a tail: 48 rows a group 259 us, this 245; 500 rows
     // 773 and 680.)
+    // The tile it waits for may come after many that it has nothing to do with,
+    // longer than a wait's limit (the other roles wait for one tile at most).
     int total = 0;
     uint32_t used = 0;  // phase bit of each barrier
     while (uniform(walk.next(p, s_off, s_pre))) {
@@ -558,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int stage = (total + place) % STAGES;
       total += nk;
       if (place == nk) continue;
-      if (!uniform(mbar_wait(&tail[stage], (used >> stage) & 1u, abort))) {
+      if (!uniform(mbar_wait_turn(&tail[stage], (used >> stage) & 1u, begun, abort))) {
         if (lane == 0) give_up(p, abort);
         break;
       }
