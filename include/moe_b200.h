@@ -294,8 +294,12 @@ typedef enum {
  *   All pointers belong to the current device.
  *   status: optional device int32, OR-ed into (the caller zeroes it): bit 2
  *     if an entry of off is negative, falls below its predecessor or lies
- *     beyond `rows` (the group it starts or ends counts as empty, its
- *     outputs are left as they were), bit 1 if a device-side wait timed out.
+ *     beyond `rows`, bit 1 if a device-side wait timed out.  A group that ends
+ *     below its start, or starts or ends outside 0..rows, counts as empty and
+ *     its outputs are left as they were.  In moe_grouped_gemm and
+ *     moe_grouped_gemm_dgrad so does one that starts below an earlier entry in
+ *     0..rows: its rows may be another group's too, and a row has one output.
+ *     Its weight gradient is that of the rows it names.
  *   stream: cudaStream_t (NULL = legacy default stream).
  *
  * moe_grouped_gemm:        y[p, n]    = act(sum_k x[p, k] w[e(p), n, k])

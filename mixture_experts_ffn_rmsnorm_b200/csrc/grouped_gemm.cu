@@ -43,6 +43,8 @@
 // (5.1).
 #include <cuda_fp16.h>
 
+#include <climits>
+
 #include "handle_free.h"
 #include "moe_internal.h"
 #include "ptx_pair.cuh"
@@ -376,10 +378,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   {
     const int e = threadIdx.x;
     int n = 0;
+    bool bad = false;
     if (e < p.groups) {
       const int a = p.off[e], b = p.off[e + 1];
       const bool good = a >= 0 && a <= b && b <= p.rows;
       if (!good && p.status && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
+      bad = !good;
       const int cnt = good ? b - a : 0;
       s_off[e] = a;
       if (e + 1 == p.groups) s_off[p.groups] = b;
@@ -393,9 +397,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int up = __shfl_up_sync(0xffffffffu, n, d);
       if (lane >= d) n += up;
     }
-    if (lane == 31) s_scan[warp] = n;
+    // (the sign says that the warp has met a bad entry)
+    const bool met = M != kWgrad && __any_sync(0xffffffffu, bad);
+    if (lane == 31) s_scan[warp] = met ? n | INT_MIN : n;
     __syncthreads();
-    for (int i = 0; i < warp; ++i) n += s_scan[i];
+    bool fell = met;
+    for (int i = 0; i < warp; ++i) {
+      n += s_scan[i] & INT_MAX;
+      fell |= M != kWgrad && s_scan[i] < 0;
+    }
+    // Where `off` falls, a group may begin below the end of one before it.  The
+    // rows they share have one owner, the first: the later group counts as empty.
+    // (A weight gradient's groups share no output.)  Threads whose own group or
+    // one before it is bad add up again, each by itself; a barrier that carries
+    // the flag cost every launch 0.2 us.
+    if (fell && e < p.groups) {
+      n = 0;
+      for (int i = 0, top = 0; i <= e; ++i) {
+        const int a = s_off[i], b = s_off[i + 1];
+        if (a >= top && a <= b && b <= p.rows) n += (b - a + NB - 1) / NB;
+        if (a <= p.rows) top = max(top, a);
+      }
+    }
     if (e == 0) s_pre[0] = 0;
     if (e < p.groups) s_pre[e + 1] = n;
   }
