@@ -715,6 +715,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = 0x38383838u;  // the tokens' scales: ones
     tmem_st_32x32b_x16(quarter + kColSfb, v);
+    tmem_st_wait();  // (a CTA without units frees the columns next)
     int stage = 0, it = 0;
     uint32_t phase = 0;
     for (int u = u0, two; u < u1; u += two, ++it) {
