@@ -593,12 +593,13 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
           // digits count halves: times 2^(1 - s), in whatever range the factors lie
           const double unscale =
               __longlong_as_double((long long)(1023 + 1 - S.shift[b][n]) << 52);
-          v = float(double(v) * unscale * double(s2));
+          double sum = double(v) * unscale;
           if (r < valid && ok && !S.abort) {
             const long long src = p.per_slot ? rows[n] : rows[n] / p.top_k;
             if (S.odd[b][n])
-              v += s2 * odd_part<BF16>(p, static_cast<const uint16_t*>(p.x) + src * p.ldx,
-                                       (long long)(e)*p.N + n0 + r);
+              sum += odd_part<BF16>(p, static_cast<const uint16_t*>(p.x) + src * p.ldx,
+                                    (long long)(e)*p.N + n0 + r);
+            v = float(sum * double(s2));
             if (p.relu2) v = v <= 0.f ? 0.f : v * v;  // NaN stays NaN
             const long long o = rows[n] * p.ldy + n0 + r;
             if constexpr (BF16)

@@ -41,3 +41,24 @@ def test_launches_with_idle_ctas():
         for j, e in enumerate(ids):
             want = (x.double() @ W[e].T).to(torch.bfloat16) if 0 <= e < E else torch.zeros_like(ys[0][:, j])
             assert all(torch.equal(y[:, j] + 0.0, want + 0.0) for y in ys)
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "fp16"))
+def test_infinite_and_nan_factors_follow_the_formula(dtype):
+    # s2 times a sum that is infinite, zero, finite or NaN, in the order of the formula
+    inf, nan = float("inf"), float("nan")
+    E, N, K = 4, 16, 32
+    w = torch.full((E, N, K // 2), 0x22, dtype=torch.uint8, device="cuda")  # ones
+    w[:, 3:6] = 0xAA  # -1
+    w[:, 6:9] = 0x00
+    s2 = torch.tensor([inf, -inf, nan, 0.0], device="cuda")
+    x = torch.zeros(5, K, dtype=DT[dtype], device="cuda")
+    x[0, 0], x[1, 1], x[2, 2], x[3, 3] = inf, -inf, 2.0, nan
+    idx = torch.arange(E, dtype=torch.int32, device="cuda").repeat(5, 1)
+    y = torch.full((5, E, N), 7.0, dtype=DT[dtype], device="cuda")
+    moe.nvfp4_gemv(x, idx, w, ones(E, N, K // 16), s2, y)
+    for t in range(5):
+        # one non-zero element at most: its product with the weight, or 0
+        k = min(t, 3)
+        want = (x[t, k].double() * values(w)[:, :, k]) * s2.double().view(E, 1)
+        torch.testing.assert_close(y[t].double(), want, rtol=0, atol=0, equal_nan=True)
