@@ -360,10 +360,14 @@ MOE_API moe_status moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const vo
  *   All pointers belong to the current device.
  *   status: optional device int32, OR-ed into (the caller zeroes it): bit 2
  *      for an id outside [0, num_experts), bit 1 if a wait timed out.
- * Weights and scales are exact, an element of x counts to 2^-22 of its row's
- * largest, sums are float32 and the result is rounded once.  Infinities and
- * NaN behave as in the formula (a row that holds one takes a slow path).
- * The weights are read once per 4 rows of an expert.
+ * Weights, scales and the elements of x count in full, whatever stands beside
+ * them; sums are float32 and the result is rounded once.  Infinities and NaN
+ * behave as in the formula.  (A row takes a slower path for those and, in BF16,
+ * for elements below 2^-37 of its largest.)
+ * An expert's weights are read once per 1, 2 or 4 of its rows: 1 row where
+ * num_tokens * top_k <= num_experts / 4, 2 rows below 3 * num_experts, 4 above;
+ * fewer for K above 3840 (4 rows) and 6400 (2 rows), and never more than the
+ * power of two at num_tokens.
  *
  * The call keeps no state and uses no workspace: it allocates nothing, may be
  * captured in a CUDA graph and may overlap in time with others.  y must not

@@ -11,15 +11,18 @@
 // weights: 38 us where the bytes take 17.6, 8 tokens over 39 experts), so the
 // block-scaled tensor cores (tcgen05.mma kind::mxf4nvf4, scale vectors of 16)
 // take the weights and their scales as they are stored.  Their other operand
-// is E2M1 too, and a token row becomes one exactly enough in digits: with a
-// power of two of its own, 2^s, a row's elements are whole numbers
-// X = round(2^s x) of magnitude at most 2^22 (the largest at least 2^21), and
-// X = sum_i d_i 8^i with eight digits d_i in -4..3, each an E2M1 value
-// (in halves).  Row n of the other operand is digit n % 8 of token n / 8;
-// eight accumulator columns join as sum_i 8^i acc_i.  An element is off by at
-// most 2^-22 of its row's largest, below what the 16-bit result shows.
-// Infinities and NaN have no digits: they count as zero there and are added
-// in the epilogue from the stored weights.
+// is E2M1 too, and a token row becomes one exactly, in digits: with a power of
+// two of its own, 2^s, a row's elements are whole numbers X = 2^s x of
+// magnitude below 2^46 (the largest at least 2^45), and X = sum_i d_i 8^i with
+// sixteen digits d_i in -4..3, each an E2M1 value (in halves).  Row n of the
+// other operand is digit n % 16 of token n / 16; sixteen accumulator columns
+// join as sum_i 8^i acc_i.  Every FP16 row fits (2^15 down to 2^-24), and of a
+// BF16 row every element down to 2^-38 of its largest.  What does not fit
+// (smaller ones, infinities and NaN) has no digits: it counts as zero there and
+// is added in the epilogue from the stored weights.  So a token's
+// elements count in full, whatever stands beside them.  (Eight digits, half the
+// columns, round to 2^-22 of the row's largest: with an FP16 60000 at a weight
+// of zero the outputs of elements around 0.1 were off by 4 %.)
 //
 // Layout: routed rows of one expert share passes of up to 4 rows over its
 // matrix.  All passes' blocks of 64 weight rows ("units") form one list, cut
@@ -39,9 +42,10 @@
 //   warps 12-19 the token rows' digits, a pass ahead of its MMAs.
 // Results do not depend on the grid.
 //
-// Measured (one B200, graph replay): one token, six experts of 2688 x 1856, 8.5
-// us (17 MB; launch 2.2 us, passes, digits and the MMAs of one tile follow one
-// another); 8 tokens, about 39 experts of 1856 x 2688, 25 us (4.6 TB/s).
+// Measured (one B200, a graph of eight calls with routings of their own): one
+// token, six experts of 2688 x 1856, 9.4 us (17 MB; launch 2.2 us, passes, digits
+// and the MMAs of one tile follow one another); 8 tokens, about 41 experts of 1856 x
+// 2688, 26.0 us (4.4 TB/s).
 #include <cuda_fp16.h>
 
 #include "handle_free.h"
@@ -53,21 +57,19 @@ namespace {
 constexpr int kGemvThreads = 672;
 constexpr int kProducer = 20;  // warp
 constexpr int kUnitRows = 64;
-constexpr int kDigits = 8;
+constexpr int kHalf = 8;            // digits of 24 bits
+constexpr int kDigits = 2 * kHalf;
 constexpr int kMaxPassRows = 4;
 constexpr int kStageK = 256;         // inputs of a stage: 128 bytes a row
 constexpr int kStageBytes = 128 * 128;  // a stage's weights
 constexpr int kMaxStages = 12;
 constexpr int kMaxRows = MOE_NVFP4_MAX_ROWS;
 constexpr int kGemvSmemMax = 232448;
-// TMEM columns: two accumulators (of kChains each), the tokens' scales (ones),
-// the stages' scales (16 columns each: 4 bytes of a row per 64 inputs, 4 x 32 rows)
+// TMEM columns: two accumulators (of a chain for each MMA warp), the tokens'
+// scales (ones), the stages' scales (16 columns each: 4 bytes of a row per 64
+// inputs, 4 x 32 rows)
 constexpr int kChains = 4;  // MMA warps, at most
-constexpr uint32_t kAccCols = kMaxPassRows * kDigits;
-constexpr uint32_t kColSfb = 2 * kChains * kAccCols;
-constexpr uint32_t kColSfa = kColSfb + 16;
-constexpr uint32_t kTmemCols = 512;
-static_assert(kColSfa + kMaxStages * 16 <= kTmemCols, "");
+constexpr int kTmemCols = 512;
 constexpr int kConverters = 8 * 32;  // threads that write digits
 
 struct GemvArgs {
@@ -87,7 +89,8 @@ struct GemvArgs {
   long long ldy;
   int* status;
   int rp;      // rows of a pass, at most (1, 2 or 4)
-  int xrows;   // digit rows kept in shared memory: max(rp * 8, 16)
+  int xrows;   // their digit rows: rp * 16, also an accumulator's columns
+  int col_sfb;  // TMEM column of the tokens' scales; the stages' follow 16 later
   int stages;
   int issuers;    // MMA warps (3 or 4); divides stages
   int xbufs;      // passes whose digits are in shared memory (1 or 2)
@@ -105,11 +108,10 @@ struct Setup {
   int count[MOE_MAX_EXPERTS];
   int first[MOE_MAX_EXPERTS];
   int passes;
-  int xrow[2][kMaxPassRows];   // token rows in each digit buffer
-  int shift[2][kMaxPassRows];  // their s
-  int odd[2][kMaxPassRows];    // the row holds an infinity or a NaN
-  float amax[kMaxPassRows][8];
-  int bad[kMaxPassRows][8];
+  int xrow[2][kMaxPassRows];      // token rows in each digit buffer
+  int top[2][kMaxPassRows];       // their largest exponents
+  uint32_t odd[2][kMaxPassRows];  // their blocks of 256 that hold elements without digits
+  uint32_t amax[kMaxPassRows][8];
   int changed;  // the last pass whose token rows differ from those of its buffer
   volatile int abort;
 };
@@ -234,35 +236,26 @@ __device__ __forceinline__ void group_rows(const GemvArgs& p, Setup& S) {
   }
 }
 
-// Eight elements of a token row in float32.
+// The 16-bit types' fields: mantissa bits, the exponent of infinities and NaN,
+// and the places by which the mantissa of a row's largest exponent is shifted up.
 template <bool BF16>
-__device__ __forceinline__ void to_float8(const uint4& u, float (&v)[8]) {
+struct Half16 {
+  static constexpr int kMant = BF16 ? 7 : 10;
+  static constexpr int kExpMax = BF16 ? 255 : 31;
+  static constexpr int kBias = BF16 ? 127 : 15;
+  static constexpr int kTop = 45 - kMant;  // the largest element below 2^46
+  static constexpr int kUnit = 45 + kBias;  // s = kUnit - the largest exponent
+};
+
+// The largest finite magnitudes (as bits) of eight elements into m, two at a time.
+template <bool BF16>
+__device__ __forceinline__ void amax8(const uint4& u, uint32_t& m) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if constexpr (BF16) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  }
-}
-
-__device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.4028235e38f; }
-
-// Their largest finite magnitude into m; bad: one is not finite.
-template <bool BF16>
-__device__ __forceinline__ void amax8(const uint4& u, float& m, int& bad) {
-  float v[8];
-  to_float8<BF16>(u, v);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const bool f = finite(v[i]);
-    m = fmaxf(m, f ? fabsf(v[i]) : 0.f);
-    bad |= !f;
+    const uint32_t a = w[i] & 0x7FFF7FFFu;
+    const uint32_t over = (a + (0x00010001u << Half16<BF16>::kMant)) & 0x80008000u;  // not finite
+    m = __vmaxu2(m, a & ~((over >> 15) * 0xFFFFu));
   }
 }
 
@@ -270,20 +263,53 @@ __device__ __forceinline__ float pow2(int e) {  // e in -126..127
   return __uint_as_float(uint32_t(e + 127) << 23);
 }
 
-// The E2M1 codes of the eight balanced base-8 digits of X (|X| <= 2^22), digit
-// i in nibble i.  With U = X + 4 (1 + 8 + ... + 8^7), digit i is
-// ((U >> 3 i) & 7) - 4.
-__device__ __forceinline__ uint32_t digit_codes(int X) {
-  uint32_t t = uint32_t(X + 9586980);
+// The E2M1 codes of the five balanced base-8 digits of V (0 <= V < 2^13), digit i
+// in nibble i, all signs flipped where `flip` is 0x88888.  With U = V + 4 (1 + 8 +
+// ... + 8^4), digit i is ((U >> 3 i) & 7) - 4.
+__device__ __forceinline__ uint32_t digit_codes(uint32_t V, uint32_t flip) {
+  uint32_t t = V + 18724u;
   // 3-bit fields to nibbles
-  t = (t & 0x00000FFFu) | ((t & 0x00FFF000u) << 4);
-  t = (t & 0x003F003Fu) | ((t & 0x0FC00FC0u) << 2);
-  t = (t & 0x07070707u) | ((t & 0x38383838u) << 1);
+  t = (t & 0x0FFFu) | ((t & 0x7000u) << 4);
+  t = (t & 0x7003Fu) | ((t & 0x0FC0u) << 2);
+  t = (t & 0x70707u) | ((t & 0x3838u) << 1);
   // t - 4 as sign and magnitude (in halves): 4..7 -> 0..3, 0..3 -> -4..-1
-  const uint32_t s = ~t & 0x44444444u;
+  const uint32_t s = ~t & 0x44444u;
   const uint32_t neg = s >> 2;
-  const uint32_t mag = ((t ^ (neg * 3u)) & 0x33333333u) + neg;
-  return mag | (s << 1);
+  const uint32_t mag = ((t ^ (neg * 3u)) & 0x33333u) + neg;
+  return (mag | (s << 1)) ^ flip;
+}
+
+// Has an element no digits?  Infinities and NaN, and in a BF16 row what may end
+// below the lowest digit's unit (bits: without the sign; least: of the smallest
+// element that has digits, see below).
+template <bool BF16>
+__device__ __forceinline__ bool no_digits(uint32_t bits, uint32_t least) {
+  return bits >= uint32_t(Half16<BF16>::kExpMax) << Half16<BF16>::kMant ||
+         (BF16 && bits < least && bits != 0);
+}
+
+// An element's mantissa lies max(exponent, 1) - top + kTop places above the unit,
+// top the row's largest such exponent: none below exponent top - kTop.
+template <bool BF16>
+__device__ __forceinline__ uint32_t least_bits(int top) {
+  using H = Half16<BF16>;
+  return top > H::kTop + 1 ? uint32_t(top - H::kTop) << H::kMant : 0u;
+}
+
+// The codes of an element's sixteen digits, upper and lower eight.
+template <bool BF16>
+__device__ __forceinline__ void element_codes(uint32_t bits, int top, bool none, uint32_t& hi,
+                                              uint32_t& lo) {
+  using H = Half16<BF16>;
+  const int ex = int(bits >> H::kMant) & H::kExpMax;
+  uint32_t mant = (bits & ((1u << H::kMant) - 1u)) | (ex ? 1u << H::kMant : 0u);
+  mant = none ? 0u : mant;
+  const int s = mant ? max(ex, 1) + H::kTop - top : 0;
+  const int q = (s * 43) >> 7;  // s / 3
+  const uint64_t c = uint64_t(digit_codes(mant << (s - 3 * q), (bits & 0x8000u) ? 0x88888u : 0u))
+                     << (4 * q);
+  hi = uint32_t(c >> 32);
+  lo = uint32_t(c);
 }
 
 // 8 x 8 nibbles: w[i] nibble j <-> w[j] nibble i.
@@ -348,21 +374,26 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-// What the infinities and NaN of a token row add to weight row `row`.
+// What the elements without digits in the 256-wide blocks `odd` of a token row add
+// to weight row `row`, in ascending order.
 template <bool BF16>
-__device__ __noinline__ float odd_part(const GemvArgs& p, const uint16_t* x, long long row) {
-  float sum = 0.f;
-  for (int k = 0; k < p.K; ++k) {
-    const uint32_t b = x[k];
-    const float v = BF16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half(uint16_t(b)));
-    if (finite(v)) continue;
-    const uint32_t code = (p.w[row * (p.K / 2) + k / 2] >> (4 * (k & 1))) & 15;
-    const uint32_t m = code & 7;
-    const float mag = m < 2 ? 0.5f * m : (1.f + 0.5f * (m & 1)) * pow2(int(m >> 1) - 1);
-    const uint32_t e4 = p.scale[row * (p.K / 16) + k / 16];
-    const float sc = (e4 & 0x78) ? (1.f + (e4 & 7) / 8.f) * pow2(int(e4 >> 3 & 15) - 7)
-                                 : (e4 & 7) * pow2(-9);
-    sum += v * ((code & 8) ? -mag : mag) * sc;
+__device__ __noinline__ double odd_part(const GemvArgs& p, const uint16_t* x, uint32_t odd,
+                                        uint32_t least, long long row) {
+  double sum = 0.;
+  for (; odd; odd &= odd - 1) {
+    const int k0 = (__ffs(odd) - 1) * 256;
+    for (int k = k0; k < min(k0 + 256, p.K); ++k) {
+      const uint32_t b = x[k];
+      if (!no_digits<BF16>(b & 0x7FFFu, least)) continue;
+      const float v = BF16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half(uint16_t(b)));
+      const uint32_t code = (p.w[row * (p.K / 2) + k / 2] >> (4 * (k & 1))) & 15;
+      const uint32_t m = code & 7;
+      const float mag = m < 2 ? 0.5f * m : (1.f + 0.5f * (m & 1)) * pow2(int(m >> 1) - 1);
+      const uint32_t e4 = p.scale[row * (p.K / 16) + k / 16];
+      const float sc = (e4 & 0x78) ? (1.f + (e4 & 7) / 8.f) * pow2(int(e4 >> 3 & 15) - 7)
+                                   : (e4 & 7) * pow2(-9);
+      sum += double(v) * double(((code & 8) ? -mag : mag) * sc);
+    }
   }
   return sum;
 }
@@ -381,7 +412,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
   uint8_t* xs = ring + p.stages * kStageBytes;    // the digits
   const int nst = (p.K + kStageK - 1) / kStageK;  // stages of a tile
   const int xblock = p.xrows * 128;               // digit rows of one stage's inputs
-  uint8_t* raw = xs + p.xbufs * nst * xblock;           // tiles' scales as they are stored
+  uint8_t* raw = xs + p.xbufs * nst * xblock;     // tiles' scales as they are stored
   const int row_bytes = p.K / 16;
   const uint32_t ring_u32 = smem_u32(ring), xs_u32 = smem_u32(xs);
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -425,7 +456,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = tmem_slot, col_sfb = uint32_t(p.col_sfb);
   // rows without an expert get zeros
   for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
     if (S.id[r] >= 0) continue;
@@ -510,9 +541,8 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
           if (!uniform(wait_for(p, &xfull[passes % p.xbufs], (passes / p.xbufs) & 1, &S.abort)))
             break;
         }
-        const int cols = max(16, (uniform(int(S.pass_n[pass])) * kDigits + 15) & ~15);
-        const uint32_t idesc = nvfp4_idesc(cols);
-        const uint32_t d = tmem + uint32_t((it & 1) * kChains + warp) * kAccCols;
+        const uint32_t idesc = nvfp4_idesc(uniform(int(S.pass_n[pass])) * kDigits);
+        const uint32_t d = tmem + uint32_t(((it & 1) * p.issuers + warp) * p.xrows);
         const uint32_t xb = xs_u32 + passes % p.xbufs * nst * xblock;
         if (!uniform(wait_for(p, &tempty[it & 1], ((it >> 1) & 1) ^ 1u, &S.abort))) break;
         tc_fence_after();
@@ -522,7 +552,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
                        wait_for(p, &sf_full[stage], phase, &S.abort));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sfa = tmem + kColSfa + stage * 16;
+          const uint32_t sfa = tmem + col_sfb + 16 + stage * 16;
           const int steps = min(4, (p.K - k * kStageK + 63) / 64);
           const uint64_t ad = smem_desc_k_sw128(ring_u32 + stage * kStageBytes);
           const uint64_t bd = smem_desc_k_sw128(xb + k * xblock);
@@ -530,7 +560,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (j < steps)
-                umma_nvfp4(d, ad + j * 2, bd + j * 2, idesc, sfa + j * 4, tmem + kColSfb,
+                umma_nvfp4(d, ad + j * 2, bd + j * 2, idesc, sfa + j * 4, tmem + col_sfb,
                            k > k0 || j > 0);
             umma_commit(&empty[stage]);
           }
@@ -571,41 +601,48 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
         const bool ok = wait_for(p, &tfull[it & 1], (it >> 1) & 1, &S.abort);
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t(cw * 32) << 16) +
-                           uint32_t(it & 1) * kChains * kAccCols;
+                           uint32_t((it & 1) * p.issuers * p.xrows);
+        const int chain0 = int(uint32_t(it * nst) % uint32_t(p.issuers));  // of the tile's first stage
         for (int n = 0; n < n_rows && cw * 32 < valid; ++n) {
           // chain c: the stages c, c + issuers, ... of the tile
           uint32_t acc[kChains][kDigits];
 #pragma unroll
           for (int c = 0; c < kChains; ++c) {
-            const uint32_t w = c < chains ? uint32_t(it * nst + c) % p.issuers : 0;
-            tmem_ld_32x32b_n<kDigits>(d + w * kAccCols + uint32_t(n * kDigits), acc[c]);
+            int w = c < chains ? chain0 + c : 0;
+            w = w >= p.issuers ? w - p.issuers : w;
+            tmem_ld_32x32b_x16(d + uint32_t(w * p.xrows + n * kDigits), acc[c]);
           }
           tmem_ld_wait_regs(acc);
-          float v = 0.f;
+          float v[2];
 #pragma unroll
-          for (int i = kDigits - 1; i >= 0; --i) {
-            float t = __uint_as_float(acc[0][i]);
+          for (int h = 0; h < 2; ++h) {
+            v[h] = 0.f;
 #pragma unroll
-            for (int c = 1; c < kChains; ++c)
-              if (c < chains) t += __uint_as_float(acc[c][i]);
-            v = fmaf(v, 8.f, t);
+            for (int i = kHalf - 1; i >= 0; --i) {
+              float t = __uint_as_float(acc[0][h * kHalf + i]);
+#pragma unroll
+              for (int c = 1; c < kChains; ++c)
+                if (c < chains) t += __uint_as_float(acc[c][h * kHalf + i]);
+              v[h] = fmaf(v[h], 8.f, t);
+            }
           }
           // digits count halves: times 2^(1 - s), in whatever range the factors lie
           const double unscale =
-              __longlong_as_double((long long)(1023 + 1 - S.shift[b][n]) << 52);
-          double sum = double(v) * unscale;
+              __longlong_as_double((long long)(1024 - Half16<BF16>::kUnit + S.top[b][n]) << 52);
+          double sum = double(fmaf(v[1], 16777216.f, v[0])) * unscale;
           if (r < valid && ok && !S.abort) {
             const long long src = p.per_slot ? rows[n] : rows[n] / p.top_k;
             if (S.odd[b][n])
               sum += odd_part<BF16>(p, static_cast<const uint16_t*>(p.x) + src * p.ldx,
+                                    S.odd[b][n], least_bits<BF16>(S.top[b][n]),
                                     (long long)(e)*p.N + n0 + r);
-            v = float(sum * double(s2));
-            if (p.relu2) v = v <= 0.f ? 0.f : v * v;  // NaN stays NaN
+            float out = float(sum * double(s2));
+            if (p.relu2) out = out <= 0.f ? 0.f : out * out;  // NaN stays NaN
             const long long o = rows[n] * p.ldy + n0 + r;
             if constexpr (BF16)
-              static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
+              static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(out);
             else
-              static_cast<__half*>(p.y)[o] = __float2half_rn(v);
+              static_cast<__half*>(p.y)[o] = __float2half_rn(out);
           }
           __syncwarp();
         }
@@ -640,56 +677,57 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
         const int k0 = part * 256 + lane * 8, kstep = per * 256;
         uint4 held[2];
         if (want >= 0) {
-          float m = 0.f;
-          int bad = 0;
+          uint32_t m = 0;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             held[i] = k0 + i * kstep < p.K
                           ? *reinterpret_cast<const uint4*>(xr + k0 + i * kstep)
                           : make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) amax8<BF16>(held[i], m, bad);
+          for (int i = 0; i < 2; ++i) amax8<BF16>(held[i], m);
           for (int k = k0 + 2 * kstep; k < p.K; k += kstep)
-            amax8<BF16>(*reinterpret_cast<const uint4*>(xr + k), m, bad);
-#pragma unroll
-          for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-          bad = __any_sync(0xffffffffu, bad);
+            amax8<BF16>(*reinterpret_cast<const uint4*>(xr + k), m);
+          m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
           if (lane == 0) {
             S.amax[n][part] = m;
-            S.bad[n][part] = bad;
+            if (part == 0) S.odd[b][n] = 0;
           }
         }
         named_barrier(1, kConverters);
         if (want >= 0) {
-          float m = 0.f;
-          int bad = 0;
-          for (int i = 0; i < per; ++i) {
-            m = fmaxf(m, S.amax[n][i]);
-            bad |= S.bad[n][i];
-          }
-          // the largest magnitude to [2^21, 2^22); a float32's exponent, or a subnormal's
-          const uint32_t mb = __float_as_uint(m);
-          const int ex = mb >> 23 ? int(mb >> 23) - 127 : -118 - __clz(mb | 1u);
-          const int sh = mb ? 21 - ex : 0;
-          const float f1 = pow2(sh / 2), f2 = pow2(sh - sh / 2);
+          using H = Half16<BF16>;
+          uint32_t m = 0;
+          for (int i = 0; i < per; ++i) m = max(m, S.amax[n][i]);
+          // the largest exponent's mantissas end 2^kTop above the lowest digit's unit
+          const int top = max(int(m >> H::kMant), 1);
+          const uint32_t least = least_bits<BF16>(top);
           if (lane == 0 && part == 0) {
             S.xrow[b][n] = want;
-            S.shift[b][n] = sh;
-            S.odd[b][n] = bad;
+            S.top[b][n] = top;
           }
           auto put = [&](int k, const uint4& u) {
-            uint32_t w[8];
-            float v[8];
-            to_float8<BF16>(u, v);
+            const uint32_t x2[4] = {u.x, u.y, u.z, u.w};
+            uint32_t hi[8], lo[8], low = 0;
+            bool odd = false;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              w[i] = digit_codes(finite(v[i]) ? __float2int_rn(v[i] * f1 * f2) : 0);
-            transpose_nibbles(w);
-            // digit i of eight inputs: 4 bytes of row n * 8 + i, swizzled as TMA would
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t bits = (x2[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
+              const bool none = no_digits<BF16>(bits & 0x7FFFu, least);
+              odd |= none;
+              element_codes<BF16>(bits, top, none, hi[i], lo[i]);
+              low |= lo[i];
+            }
+            if (odd) atomicOr(&S.odd[b][n], 1u << (k / 256));
+            transpose_nibbles(hi);
+            if (__any_sync(0xffffffffu, low)) transpose_nibbles(lo);  // (rare in BF16 rows)
+            // digit i of eight inputs: 4 bytes of row n * 16 + i, swizzled as TMA would
             uint8_t* dst = xs + (b * nst + k / kStageK) * xblock + n * kDigits * 128 + (lane & 3) * 4;
 #pragma unroll
-            for (int i = 0; i < kDigits; ++i)
-              *reinterpret_cast<uint32_t*>(dst + i * 128 + ((lane >> 2) ^ i) * 16) = w[i];
+            for (int i = 0; i < kHalf; ++i) {
+              uint8_t* d = dst + i * 128 + ((lane >> 2) ^ i) * 16;
+              *reinterpret_cast<uint32_t*>(d) = lo[i];
+              *reinterpret_cast<uint32_t*>(d + kHalf * 128) = hi[i];
+            }
           };
           // zeros behind K, to the end of the last stage
           // (one copy of the code: it runs cold)
@@ -715,7 +753,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     uint32_t v[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = 0x38383838u;  // the tokens' scales: ones
-    tmem_st_32x32b_x16(quarter + kColSfb, v);
+    tmem_st_32x32b_x16(quarter + col_sfb, v);
     tmem_st_wait();  // (a CTA without units frees the columns next)
     int stage = 0, it = 0;
     uint32_t phase = 0;
@@ -742,7 +780,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
         }
         wait_for(p, &empty[stage], phase ^ 1u, &S.abort);
         tc_fence_after();
-        tmem_st_32x32b_x16(quarter + kColSfa + stage * 16, v);
+        tmem_st_32x32b_x16(quarter + col_sfb + 16 + stage * 16, v);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -852,34 +890,48 @@ extern "C" moe_status moe_nvfp4_gemv(const void* x, int64_t ldx, int32_t x_per_s
   a.y = y;
   a.ldy = ldy;
   a.status = status;
-  // Rows of a pass: as many as an expert can have when ids are distinct, at
-  // most 4 (their digits take shared memory from the ring and accumulator
-  // columns), fewer where the digits would leave less than four stages.
-  a.rp = num_tokens > 2 ? kMaxPassRows : num_tokens;
-  if (a.rp > 2 && a.R < num_experts) a.rp = 2;  // experts with more are rare
+  // Rows of a pass: more rows share one read of the weights, but each takes
+  // shared memory from the ring and accumulator columns.  128 experts of 2688 x
+  // 1856, k = 6, us with passes of 1 / 2 / 4 rows, uniform routing (and with
+  // popularity rank^-1.2): 4 tokens 16.1 / 17.8 / 19.0 (15.2 / 17.4 / 21.3), 8 tokens
+  // 26.4 / 26.6 / 30.5 (24.2 / 22.6 / 31.2), 16 tokens 44.8 / 39.1 / 43.3 (36.6 / 31.9 /
+  // 39.1), 32 tokens 82 / 57.1 / 61.4 (65 / 48.5 / 50.3), 64 tokens 162 / 105 / 75.5 (123
+  // / 82.9 / 70.3), 128 tokens 279 / 176 / 132 (237 / 145 / 118).
+  a.rp = 4 * a.R <= num_experts ? 1 : a.R < 3 * num_experts ? 2 : kMaxPassRows;
+  if (a.rp > num_tokens) a.rp = num_tokens > 1 ? 2 : 1;  // ids of a token are distinct, as a rule
+  // What shares the memory: digits of one or two passes, scales of one or two
+  // tiles, the ring.  The first that leaves the ring its stages; fewer rows a pass
+  // where none does.  (One token, 2688 x 1856: 9 stages and one tile's scales 9.5
+  // us, 8 and two tiles' 9.7.  8 tokens: 6 stages and two passes' digits 26.5, 8
+  // and one pass's 28.6.)
+  struct Share {
+    int xbufs, raws, stages;
+  };
+  constexpr Share kShares[] = {{2, 2, 9}, {2, 1, 9}, {2, 2, 6}, {2, 1, 6}, {1, 2, 6}, {1, 1, 4}};
   const int nst = (K + kStageK - 1) / kStageK;
-  const int room = kGemvSmemMax - kGemvStatic - 1024;
   a.raw_bytes = 128 * (K / 16) + 32;
-  a.raws = a.xbufs = 2;
-  for (;;) {
-    a.xrows = a.rp * kDigits < 16 ? 16 : a.rp * kDigits;
-    a.stages = (room - a.xbufs * nst * a.xrows * 128 - a.raws * a.raw_bytes) / kStageBytes;
-    if (a.stages >= (a.xbufs == 2 ? 6 : 4)) break;
-    if (a.xbufs == 2)
-      a.xbufs = 1;
-    else if (a.raws == 2)
-      a.raws = 1;
-    else if (a.rp > 2)
-      a.rp /= 2;
-    else
-      break;
+  for (a.stages = 0;; a.rp /= 2) {
+    a.xrows = a.rp * kDigits;
+    for (const Share& s : kShares) {
+      a.xbufs = s.xbufs;
+      a.raws = s.raws;
+      a.stages = (kGemvSmemMax - kGemvStatic - 1024 - a.xbufs * nst * a.xrows * 128 -
+                  a.raws * a.raw_bytes) /
+                 kStageBytes;
+      if (a.stages >= s.stages) break;
+    }
+    if (a.stages >= 4 || a.rp == 1) break;
   }
-  if (a.stages > kMaxStages) a.stages = kMaxStages;
-  a.issuers = a.stages / 3 * 3 > a.stages / 4 * 4 ? 3 : 4;
+  // (three MMA warps where accumulators of 64 columns leave none for a fourth's)
+  const bool wide = a.rp == kMaxPassRows;
+  if (a.stages > (wide ? 6 : kMaxStages)) a.stages = wide ? 6 : kMaxStages;
+  a.issuers = wide || a.stages / 3 * 3 > a.stages / 4 * 4 ? 3 : 4;
   a.stages = a.stages / a.issuers * a.issuers;
+  a.col_sfb = 2 * a.issuers * a.xrows;
   const long long most = (long long)(a.R) * ((N + kUnitRows - 1) / kUnitRows);
   const int grid = int(most < sms ? most : sms);
-  const int smem = 1024 + a.stages * kStageBytes + a.xbufs * nst * a.xrows * 128 + a.raws * a.raw_bytes;
+  const int smem = 1024 + a.stages * kStageBytes + a.xbufs * nst * a.xrows * 128 +
+                   a.raws * a.raw_bytes;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == MOE_DTYPE_BF16;
   const int row_bytes = K / 16;  // of scales: even
