@@ -289,8 +289,11 @@ typedef enum {
  *   dtype: MOE_DTYPE_BF16 or MOE_DTYPE_FP16, of all operands and (except
  *     out_dtype) of the output.  Sums are float32, rounded once.  (The tensor
  *     cores truncate as they add: a sum of q products loses about q * 1e-9 of
- *     itself.  FP32 gradients are added up in pieces of 768 rows, which keeps
- *     them within 1e-6.)
+ *     itself, q * 6e-9 where all have one sign.  Sums are therefore added up in
+ *     pieces of 8192 products, FP32 gradients in pieces of 768 rows.  That keeps
+ *     16-bit results within 1e-5 of the exact sum before they are rounded, 5e-5
+ *     for one sign; and FP32 gradients within 1e-6, 5e-6 for one sign, up to 10^6
+ *     rows of a group, 2e-6 and 5e-6 at 2^24.)
  *   All pointers belong to the current device.
  *   status: optional device int32, OR-ed into (the caller zeroes it): bit 2
  *     if an entry of off is negative, falls below its predecessor or lies

@@ -97,13 +97,16 @@ struct Traits {
   static constexpr int kRound = M == kWgrad && EB == 2 ? 2 : 1;
   static constexpr int kWarpStaging = kRound * kChunk;
   static constexpr int kStagingBytes = kEpiWarps * kWarpStaging;
-  // The tensor cores truncate as they accumulate: a sum of n rows loses about
-  // n * 1e-9 of itself (measured: 9e-6 at 8192).  A 16-bit result hides that;
-  // for an FP32 one the sums start anew every 768 rows (7e-7) and are added up,
-  // rounding to nearest: two in the epilogue, which takes both accumulators
-  // then, and every two sums in memory.  (128 groups of 780 rows, 1024 x 2688:
-  // 819 us with each added up in memory, 694 with pairs.)
-  static constexpr int kSegment = EB == 4 ? 12 : 1 << 28;  // k-blocks
+  // The tensor cores truncate as they accumulate: a sum of q products loses about
+  // q * 1e-9 of itself, where all have one sign q * 6e-9 (measured: 9e-6 and 5e-5 at
+  // 8192; in one piece 2^20 products 1.2e-3 and 6.9e-3, more than an FP16 rounding).
+  // So sums start anew every 128 k-blocks, 8192 products, and the pieces are added up,
+  // rounding to nearest, in TMEM: the epilogue adds the sum so far to the next piece
+  // before it hands the accumulator back.  For an FP32 result they start anew every
+  // 768 rows (7e-7 and 4e-6): two are joined in the epilogue, which takes both
+  // accumulators then, and every two sums in memory.  (128 groups of 780 rows, 1024 x
+  // 2688: 819 us with each added up in memory, 694 with pairs.)
+  static constexpr int kSegment = EB == 4 ? 12 : 128;  // k-blocks
   // Weight gradient: a group's last k-block is loaded this many k-blocks ahead of
   // its turn, in which time the rows behind the group's last one are cleared
   // (128 groups of 500 / 333 / 261 / 135 rows, 2688 x 1856, us: 0 ahead 725 / 553
@@ -116,6 +119,7 @@ struct Traits {
   static constexpr int kBarriers = (3 * STAGES + 7) * 8;
   static constexpr int kSmem = STAGES * kStageBytes + kStagingBytes + kBarriers +
                                (2 * (MOE_MAX_EXPERTS + 1) + kThreads / 32) * 4;
+  static_assert(kSegment % KPS == 0, "");
   static_assert(!kBMN || KPS == 1, "the tail of a group is one k-block of one stage");
   static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols <= 512, "");
   static_assert(kSmem <= 232448, "");
@@ -209,6 +213,24 @@ __device__ __forceinline__ bool mbar_wait_turn(uint64_t* bar, uint32_t parity, v
     if (clock64() - t0 > kWaitLimitCycles) return false;
   }
   return true;
+}
+
+// N TMEM columns from `base + to` on, in this warp's lanes: plus those from `base +
+// from` on.
+template <int N>
+__device__ __noinline__ void add_columns(uint32_t base, uint32_t from, uint32_t to) {
+#pragma unroll 1
+  for (int j = 0; j < N; j += 16) {
+    uint32_t s[2][16];
+    tmem_ld_32x32b_x16(base + from + uint32_t(j), s[0]);
+    tmem_ld_32x32b_x16(base + to + uint32_t(j), s[1]);
+    tmem_ld_wait_regs(s);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      s[1][i] = __float_as_uint(__uint_as_float(s[0][i]) + __uint_as_float(s[1][i]));
+    tmem_st_32x32b_x16(base + to + uint32_t(j), s[1]);
+  }
+  tmem_st_wait();
 }
 
 __device__ __forceinline__ float relu2(float v) {
@@ -645,8 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cw = uniform(walk.t.c0) + int(rank) * 128 + q * 32;
       const long long row = M == kWgrad ? r0 : (long long)(uniform(walk.t.row0)) + r0;
       const long long base = (M == kWgrad ? e * p.group_stride : 0) + row * p.ldo;
-      for (int seg = 0; seg == 0 || (seg < nk && ok); seg += 2 * Tr::kSegment) {
-        const int ab = it & 1;
+      for (int seg = 0; seg == 0 || (EB == 4 && seg < nk && ok); seg += 2 * Tr::kSegment) {
+        int ab = it & 1;
         const bool two = EB == 4 && nk - seg > Tr::kSegment;  // sums to join
         if (nk > 0) {
           ok = uniform(mbar_wait(&tfull[ab], (it >> 1) & 1, abort));
@@ -654,6 +676,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (two && ok) {
             ok = uniform(mbar_wait(&tfull[ab ^ 1], (it >> 1) & 1, abort));
             ++it;
+          }
+          if (EB == 2) {
+            // the pieces of a long sum: each takes in the sum before it
+            for (int done = Tr::kSegment; done < nk && ok; done += Tr::kSegment) {
+              ok = uniform(mbar_wait(&tfull[ab ^ 1], (it >> 1) & 1, abort));
+              ++it;
+              if (!ok) break;
+              tc_fence_after();
+              if (cw < p.C)
+                for (int j0 = half * 32 * Tr::kRound; j0 < nr; j0 += 64 * Tr::kRound)
+                  add_columns<32 * Tr::kRound>(tmem_base + (uint32_t(q * 32) << 16) + uint32_t(j0),
+                                               uint32_t(ab * NB), uint32_t((ab ^ 1) * NB));
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                if (CG == 2)
+                  mbar_arrive_at(map_to_rank(smem_u32(&tempty[ab]), 0));
+                else
+                  mbar_arrive(&tempty[ab]);
+              }
+              ab ^= 1;
+            }
           }
           if (!ok) {
             if (lane == 0) give_up(p, abort);
