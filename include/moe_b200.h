@@ -313,8 +313,8 @@ typedef enum {
  *
  * The calls keep no state and use no workspace: they allocate nothing, may be
  * captured in a CUDA graph and may overlap in time.  Outputs must not overlap
- * operands.  The first call of a kind on a device does set-up; make it before
- * any stream capture.
+ * operands.  The first call of each operator on a device that has rows does its
+ * set-up, for all sizes and types; make it before any stream capture.
  *
  * Errors (nothing is launched): MOE_ERR_INVALID_CONFIG for num_experts outside
  * [1, MOE_MAX_EXPERTS], features outside [1, MOE_GROUPED_MAX_FEATURES], a bad
@@ -374,8 +374,8 @@ MOE_API moe_status moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const vo
  *
  * The call keeps no state and uses no workspace: it allocates nothing, may be
  * captured in a CUDA graph and may overlap in time with others.  y must not
- * overlap an operand.  The first call on a device does set-up; make it before
- * any stream capture.
+ * overlap an operand.  The first call on a device that has tokens does set-up, for
+ * all sizes and types; make it before any stream capture.
  *
  * Errors (nothing is launched): MOE_ERR_INVALID_CONFIG for num_experts outside
  * [1, MOE_MAX_EXPERTS], top_k outside [1, MOE_MAX_TOP_K], K outside

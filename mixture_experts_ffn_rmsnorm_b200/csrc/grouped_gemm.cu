@@ -820,17 +820,14 @@ template <Mode M, int CG, int NB, int KPS, int STAGES, int EB>
 struct Variant {
   using Tr = Traits<M, CG, NB, KPS, STAGES, EB>;
 
-  static cudaError_t launch(const GroupedArgs& a, int dev, int sms, long long max_tiles,
+  // On the current device, before the first launch: loads the kernel, too.
+  static cudaError_t set_up() {
+    return cudaFuncSetAttribute(ragged_gemm_kernel<M, CG, NB, KPS, STAGES, EB>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, Tr::kSmem);
+  }
+
+  static cudaError_t launch(const GroupedArgs& a, int sms, long long max_tiles,
                             cudaStream_t stream) {
-    // the shared memory limit, once per device
-    static std::atomic<bool> ready[kMaxDevices];
-    auto* fn = ragged_gemm_kernel<M, CG, NB, KPS, STAGES, EB>;
-    if (!ready[dev].load(std::memory_order_acquire)) {
-      const cudaError_t e =
-          cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Tr::kSmem);
-      if (e != cudaSuccess) return e;
-      ready[dev].store(true, std::memory_order_release);
-    }
     const int units = sms / CG;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(CG * (max_tiles < units ? max_tiles : units)));
@@ -846,7 +843,7 @@ struct Variant {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, fn, a);
+    return cudaLaunchKernelEx(&cfg, ragged_gemm_kernel<M, CG, NB, KPS, STAGES, EB>, a);
   }
 
   // Tiles of `groups` groups with `rows` rows in all, at most.
@@ -871,7 +868,7 @@ bool map_of(CUtensorMap* m, const Operand& o, uint32_t fmt, int box_rows, bool s
 }
 
 template <Mode M, int CG, int NB, int KPS, int STAGES, int EB>
-moe_status run_variant(GroupedArgs& a, const Operand& A, const Operand& B, int dev, int sms,
+moe_status run_variant(GroupedArgs& a, const Operand& A, const Operand& B, int sms,
                        cudaStream_t stream) {
   using V = Variant<M, CG, NB, KPS, STAGES, EB>;
   bool ok = map_of(&a.tmA, A, a.fmt, M == kFwd ? 128 : 64);
@@ -891,11 +888,28 @@ moe_status run_variant(GroupedArgs& a, const Operand& A, const Operand& B, int d
                            uint64_t(a.ldo) * EB, uint64_t(a.group_stride) * EB, 32 * V::Tr::kRound,
                            32 * EB);
   if (!ok) return MOE_ERR_CUDA;
-  if (V::launch(a, dev, sms, V::tiles_of(a), stream) != cudaSuccess) {
+  if (V::launch(a, sms, V::tiles_of(a), stream) != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
   }
   return MOE_OK;
+}
+
+// All of an operator's variants, so that a call whose sizes take another one than
+// the first call's finds it ready (inside a stream capture, say).
+template <Mode M>
+cudaError_t set_up_variants() {
+  const auto all = [](auto... v) {
+    cudaError_t e = cudaSuccess;
+    ((e = e != cudaSuccess ? e : decltype(v)::set_up()), ...);
+    return e;
+  };
+  if constexpr (M == kWgrad)
+    return all(Variant<M, 1, 128, 1, 6, 4>(), Variant<M, 2, 256, 1, 6, 4>(),
+               Variant<M, 1, 128, 1, 6, 2>(), Variant<M, 2, 256, 1, 6, 2>());
+  else
+    return all(Variant<M, 1, 64, 2, 4, 2>(), Variant<M, 2, 128, 1, 8, 2>(),
+               Variant<M, 2, 256, 1, 6, 2>());
 }
 
 // Rules every operand keeps: a leading dimension that covers the row, in
@@ -921,6 +935,14 @@ moe_status dispatch(GroupedArgs& a, const Operand& A, const Operand& B, bool out
   int dev = 0, sms = 0;
   const moe_status st = current_device(&dev, &sms);
   if (st != MOE_OK) return st;
+  static std::atomic<bool> ready[kMaxDevices];
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    if (set_up_variants<M>() != cudaSuccess) {
+      cudaGetLastError();
+      return MOE_ERR_CUDA;
+    }
+    ready[dev].store(true, std::memory_order_release);
+  }
   // Tiles a launch is likely to have: half of the groups end in a part of a
   // row tile.
   const auto tiles = [&](int cg, int nb) {
@@ -940,19 +962,19 @@ moe_status dispatch(GroupedArgs& a, const Operand& A, const Operand& B, bool out
     int nb = a.rows <= 64LL * a.groups ? 64 : a.rows <= 128LL * a.groups ? 128 : 256;
     if (nb == 256 && tiles(2, 256) < sms / 2) nb = 128;
     if (nb == 128 && tiles(2, 128) < sms / 2) nb = 64;
-    if (nb == 64) return run_variant<M, 1, 64, 2, 4, 2>(a, A, B, dev, sms, stream);
-    if (nb == 128) return run_variant<M, 2, 128, 1, 8, 2>(a, A, B, dev, sms, stream);
-    return run_variant<M, 2, 256, 1, 6, 2>(a, A, B, dev, sms, stream);
+    if (nb == 64) return run_variant<M, 1, 64, 2, 4, 2>(a, A, B, sms, stream);
+    if (nb == 128) return run_variant<M, 2, 128, 1, 8, 2>(a, A, B, sms, stream);
+    return run_variant<M, 2, 256, 1, 6, 2>(a, A, B, sms, stream);
   } else {
     // Small gradients: single CTAs and 128 x 128 tiles, four times as many (one
     // group of 571 rows, K = 856, N = 768: 8.0 us for 10.4; two of 200 rows,
     // 376 x 872: 7.1 for 9.2).
     const bool few = tiles(2, 256) < sms / 2;
     if (out_f32)
-      return few ? run_variant<M, 1, 128, 1, 6, 4>(a, A, B, dev, sms, stream)
-                 : run_variant<M, 2, 256, 1, 6, 4>(a, A, B, dev, sms, stream);
-    return few ? run_variant<M, 1, 128, 1, 6, 2>(a, A, B, dev, sms, stream)
-               : run_variant<M, 2, 256, 1, 6, 2>(a, A, B, dev, sms, stream);
+      return few ? run_variant<M, 1, 128, 1, 6, 4>(a, A, B, sms, stream)
+                 : run_variant<M, 2, 256, 1, 6, 4>(a, A, B, sms, stream);
+    return few ? run_variant<M, 1, 128, 1, 6, 2>(a, A, B, sms, stream)
+               : run_variant<M, 2, 256, 1, 6, 2>(a, A, B, sms, stream);
   }
 }
 

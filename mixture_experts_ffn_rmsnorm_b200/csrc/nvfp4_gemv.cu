@@ -804,16 +804,22 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
 // Static shared memory of the kernel, at most.
 constexpr int kGemvStatic = int(sizeof(Setup)) + 512;
 
+// All variants on the current device, before the first launch (loads the kernels,
+// too): a call of another type or width than the first one's finds its own ready.
+cudaError_t set_up_variants() {
+  cudaError_t e = cudaSuccess;
+  for (auto* fn : {nvfp4_gemv_kernel<true, 16>, nvfp4_gemv_kernel<true, 8>,
+                   nvfp4_gemv_kernel<true, 4>, nvfp4_gemv_kernel<true, 2>,
+                   nvfp4_gemv_kernel<false, 16>, nvfp4_gemv_kernel<false, 8>,
+                   nvfp4_gemv_kernel<false, 4>, nvfp4_gemv_kernel<false, 2>})
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kGemvSmemMax - kGemvStatic);
+  return e;
+}
+
 template <bool BF16, int W>
-cudaError_t launch_gemv(const GemvArgs& a, int dev, int grid, int smem, cudaStream_t stream) {
-  static std::atomic<bool> ready[kMaxDevices];
-  if (!ready[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(nvfp4_gemv_kernel<BF16, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kGemvSmemMax - kGemvStatic);
-    if (e != cudaSuccess) return e;
-    ready[dev].store(true, std::memory_order_release);
-  }
+cudaError_t launch_gemv(const GemvArgs& a, int grid, int smem, cudaStream_t stream) {
   // a programmatic dependent launch: the set-up up to pdl_wait overlaps the
   // kernel before
   cudaLaunchConfig_t cfg = {};
@@ -830,10 +836,9 @@ cudaError_t launch_gemv(const GemvArgs& a, int dev, int grid, int smem, cudaStre
 }
 
 template <int W>
-cudaError_t launch_any(bool bf16, const GemvArgs& a, int dev, int grid, int smem,
-                       cudaStream_t stream) {
-  return bf16 ? launch_gemv<true, W>(a, dev, grid, smem, stream)
-              : launch_gemv<false, W>(a, dev, grid, smem, stream);
+cudaError_t launch_any(bool bf16, const GemvArgs& a, int grid, int smem, cudaStream_t stream) {
+  return bf16 ? launch_gemv<true, W>(a, grid, smem, stream)
+              : launch_gemv<false, W>(a, grid, smem, stream);
 }
 
 }  // namespace
@@ -866,6 +871,14 @@ extern "C" moe_status moe_nvfp4_gemv(const void* x, int64_t ldx, int32_t x_per_s
   int dev = 0, sms = 0;
   const moe_status st = current_device(&dev, &sms);
   if (st != MOE_OK) return st;
+  static std::atomic<bool> ready[kMaxDevices];
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    if (set_up_variants() != cudaSuccess) {
+      cudaGetLastError();
+      return MOE_ERR_CUDA;
+    }
+    ready[dev].store(true, std::memory_order_release);
+  }
 
   GemvArgs a = {};
   const int K = in_features, N = out_features;
@@ -935,10 +948,10 @@ extern "C" moe_status moe_nvfp4_gemv(const void* x, int64_t ldx, int32_t x_per_s
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == MOE_DTYPE_BF16;
   const int row_bytes = K / 16;  // of scales: even
-  const cudaError_t err = row_bytes % 16 == 0  ? launch_any<16>(bf16, a, dev, grid, smem, cs)
-                          : row_bytes % 8 == 0 ? launch_any<8>(bf16, a, dev, grid, smem, cs)
-                          : row_bytes % 4 == 0 ? launch_any<4>(bf16, a, dev, grid, smem, cs)
-                                               : launch_any<2>(bf16, a, dev, grid, smem, cs);
+  const cudaError_t err = row_bytes % 16 == 0  ? launch_any<16>(bf16, a, grid, smem, cs)
+                          : row_bytes % 8 == 0 ? launch_any<8>(bf16, a, grid, smem, cs)
+                          : row_bytes % 4 == 0 ? launch_any<4>(bf16, a, grid, smem, cs)
+                                               : launch_any<2>(bf16, a, grid, smem, cs);
   if (err != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
