@@ -1,5 +1,6 @@
 // What the handle-free operators (grouped_gemm.cu, nvfp4_gemv.cu) share on
-// the host: the current device's properties, looked up once, and tensor maps.
+// the host: the current device's properties, looked up once, and tensor maps
+// (whose encoder moe_api.cu uses, too).
 #pragma once
 
 #include <cuda.h>

@@ -16,6 +16,7 @@
 
 #include "../../include/moe_b200.h"
 #include "decode.h"
+#include "handle_free.h"
 #include "moe_internal.h"
 
 using moe::GemmParams;
@@ -25,29 +26,11 @@ namespace {
 
 constexpr uint32_t kMagic = 0x4D6F4542u;  // "MoEB"
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn get_encode() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
-  return fn;
-}
-
 // 2-D K-major operand map: inner = K extent (elements), rows, row stride in
 // bytes; box = 128 bytes of K x box_rows rows, 128-byte swizzle, zero fill.
 bool make_map(CUtensorMap* m, const void* base, bool byte_elems, uint64_t inner, uint64_t rows,
               uint64_t row_stride_bytes, uint32_t box_rows) {
-  EncodeTiledFn enc = get_encode();
+  const moe::EncodeTiledFn enc = moe::encode_tiled();
   if (!enc) return false;
   const cuuint64_t dims[2] = {inner, rows};
   const cuuint64_t strides[1] = {row_stride_bytes};

@@ -271,15 +271,17 @@ __device__ __forceinline__ void tmem_ld_wait() {
 // type 2 = SWIZZLE_128B (bits 61-63).  The tile base must be 1024-byte
 // aligned; stepping along K inside the 128-byte row adds bytes/16 to the
 // start-address field.
-__device__ __forceinline__ uint64_t smem_desc_sw128(const void* tile) {
-  const uint64_t addr = smem_u32(tile);
+__device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t tile) {  // a shared address
   uint64_t d = 0;
-  d |= (addr >> 4) & 0x3FFFull;        // start address
-  d |= uint64_t(1) << 16;              // leading byte offset (unused)
-  d |= uint64_t(1024 >> 4) << 32;      // stride byte offset
-  d |= uint64_t(1) << 46;              // version
-  d |= uint64_t(2) << 61;              // SWIZZLE_128B
+  d |= uint64_t((tile >> 4) & 0x3FFFu);  // start address
+  d |= uint64_t(1) << 16;                // leading byte offset (unused)
+  d |= uint64_t(1024 >> 4) << 32;        // stride byte offset
+  d |= uint64_t(1) << 46;                // version
+  d |= uint64_t(2) << 61;                // SWIZZLE_128B
   return d;
+}
+__device__ __forceinline__ uint64_t smem_desc_sw128(const void* tile) {
+  return smem_desc_k_sw128(smem_u32(tile));
 }
 
 // Instruction descriptor: D f32, A/B K-major, M x N.  a_fmt/b_fmt: for

@@ -225,17 +225,6 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t tile, uint32_t b
   return d;
 }
 
-// smem_desc_sw128 (K-major, 128-byte swizzle) from a shared address.
-__device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t tile) {
-  uint64_t d = 0;
-  d |= uint64_t((tile >> 4) & 0x3FFFu);
-  d |= uint64_t(1) << 16;
-  d |= uint64_t(1024 >> 4) << 32;
-  d |= uint64_t(1) << 46;  // version
-  d |= uint64_t(2) << 61;  // SWIZZLE_128B
-  return d;
-}
-
 // make_idesc with run-time N, one 16-bit format for both operands (0 = FP16,
 // 1 = BF16) and their majorness (1 = MN-major).
 __device__ __forceinline__ uint32_t make_idesc_16(uint32_t M, uint32_t N, uint32_t fmt,
