@@ -292,8 +292,8 @@ typedef enum {
  *     itself, q * 6e-9 where all have one sign.  Sums are therefore added up in
  *     pieces of 8192 products, FP32 gradients in pieces of 768 rows.  That keeps
  *     16-bit results within 1e-5 of the exact sum before they are rounded, 5e-5
- *     for one sign; and FP32 gradients within 1e-6, 5e-6 for one sign, up to 10^6
- *     rows of a group, 2e-6 and 5e-6 at 2^24.)
+ *     for one sign; and FP32 gradients within about 1e-6, 4e-6 for one sign, up to
+ *     10^6 rows of a group, 2e-6 and 5e-6 at 2^24.)
  *   All pointers belong to the current device.
  *   status: optional device int32, OR-ed into (the caller zeroes it): bit 2
  *     if an entry of off is negative, falls below its predecessor or lies
@@ -366,7 +366,7 @@ MOE_API moe_status moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const vo
  * Weights, scales and the elements of x count in full, whatever stands beside
  * them; sums are float32 and the result is rounded once.  Infinities and NaN
  * behave as in the formula.  (A row takes a slower path for those and, in BF16,
- * for elements below 2^-37 of its largest.)
+ * for elements below 2^-38 of its largest.)
  * An expert's weights are read once per 1, 2 or 4 of its rows: 1 row where
  * num_tokens * top_k <= num_experts / 4, 2 rows below 3 * num_experts, 4 above;
  * fewer for K above 3840 (4 rows) and 6400 (2 rows), and never more than the

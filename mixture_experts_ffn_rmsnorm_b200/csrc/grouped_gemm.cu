@@ -33,14 +33,17 @@
 // at the tensor cores' full rate instead of 96 for one CTA with the same NB.
 // Every wait is bounded; a timeout sets a status bit and the CTA winds down.
 //
-// What bounds it and what it reaches (one B200, sustained, H = 2688, I = 1856,
-// 128 experts): few rows a group, the weights' stream: 8 tokens 64 us, 48 rows
-// a group 204 us (6.4 and 6.5 TB/s); many, the tensor cores under the 1000 W
-// cap: dense 8192 x 4096 x 4096 194 us (1417 TFLOP/s; in a burst 172 us), 384
-// rows a group on average but 7300 on the hottest 500 to 530 us (970 to 920).
-// Weight gradients of few rows, the writes: 48 rows a group 247 us (5.4 TB/s;
-// plain stores of zeros to the same 1.28 GB take 320), 256 rows in FP32 325 us
-// (5.1).
+// What bounds it and what it reaches (sustained, H = 2688, I = 1856, 128 experts;
+// the range over several B200s): few rows a group, the weights' stream: 8 tokens 64
+// to 69 us, 48 rows a group 204 to 221 us (6.5 to 6.0 TB/s); many, the tensor cores
+// under the 1000 W cap: dense 8192 x 4096 x 4096 194 us (1417 TFLOP/s; in a burst
+// 172 us).  384 rows a group on average but 7300 on the hottest, 504 to 563 us (970
+// to 870 TFLOP/s): light groups stream weights and heavy ones compute, one after the
+// other.  Even groups of 130 to 500 rows take 1.3 to 1.5 times the larger of both,
+// DRAM and the tensor cores each busy 60 % of the time; which role waits there has not
+// been measured.  Weight gradients of few rows, the writes: 48 rows a group 247 to
+// 268 us (5.4 to 5.0 TB/s; plain stores of zeros to the same 1.28 GB take 320), 256
+// rows in FP32 325 to 343 us.
 #include <cuda_fp16.h>
 
 #include <climits>
@@ -956,7 +959,10 @@ moe_status dispatch(GroupedArgs& a, const Operand& A, const Operand& B, bool out
     // tiles would leave SMs idle.  128 groups of K = 2688, N = 1856, forward,
     // with row tiles of 64 / 128 / 256: 1 row a group 184 / 188 / 195 us, 48
     // 206 / 209 / 216, 64 213 / 214 / 224, 80 282 / 226 / 234, 128 311 / 254 /
-    // 260, 160 413 / 338 / 295, 256 553 / 420 / 357.  One group of 2048 rows,
+    // 260, 160 413 / 338 / 295, 256 553 / 420 / 357.  The mean stands
+    // for skewed groups, too: 48 rows on average, the hottest 900, 211 / 207 / 212 us (K =
+    // 1856, N = 2688: 226 / 210 / 212); 96 on average, the hottest 1810, 263 / 231 / 235.
+    // One group of 2048 rows,
     // K = 1024, N = 512: 6.9 us with 64-row tiles, 11.3 with 256; 8192 rows, N =
     // 1024: 17.6 with 256 (132 tiles for 74 pairs).
     int nb = a.rows <= 64LL * a.groups ? 64 : a.rows <= 128LL * a.groups ? 128 : 256;
