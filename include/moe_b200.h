@@ -369,8 +369,8 @@ MOE_API moe_status moe_grouped_gemm_wgrad(const void* dy, int64_t lddy, const vo
  * for elements below 2^-38 of its largest.)
  * An expert's weights are read once per 1, 2 or 4 of its rows: 1 row where
  * num_tokens * top_k <= num_experts / 4, 2 rows below 3 * num_experts, 4 above;
- * fewer for K above 3840 (4 rows) and 6400 (2 rows), and never more than the
- * power of two at num_tokens.
+ * fewer for K above 4096 (4 rows) and 6400 (2 rows); 1 row for one token, at
+ * most 2 rows for two or three.
  *
  * The call keeps no state and uses no workspace: it allocates nothing, may be
  * captured in a CUDA graph and may overlap in time with others.  y must not

@@ -70,6 +70,9 @@ constexpr int kGemvSmemMax = 232448;
 // inputs, 4 x 32 rows)
 constexpr int kChains = 4;  // MMA warps, at most
 constexpr int kTmemCols = 512;
+constexpr int kWideChains = 3, kWideStages = 6;  // with passes of kMaxPassRows
+static_assert(2 * kChains * 2 * kDigits + 16 + kMaxStages * 16 <= kTmemCols, "");
+static_assert(2 * kWideChains * kMaxPassRows * kDigits + 16 + kWideStages * 16 <= kTmemCols, "");
 constexpr int kConverters = 8 * 32;  // threads that write digits
 
 struct GemvArgs {
@@ -916,7 +919,8 @@ extern "C" moe_status moe_nvfp4_gemv(const void* x, int64_t ldx, int32_t x_per_s
   // tiles, the ring.  The first that leaves the ring its stages; fewer rows a pass
   // where none does.  (One token, 2688 x 1856: 9 stages and one tile's scales 9.5
   // us, 8 and two tiles' 9.7.  8 tokens: 6 stages and two passes' digits 26.5, 8
-  // and one pass's 28.6.)
+  // and one pass's 28.6.  64 tokens, 4096 x 1024: 3 stages and 4 rows a pass 93, 4
+  // and 2 rows 118.)
   struct Share {
     int xbufs, raws, stages;
   };
@@ -933,12 +937,14 @@ extern "C" moe_status moe_nvfp4_gemv(const void* x, int64_t ldx, int32_t x_per_s
                  kStageBytes;
       if (a.stages >= s.stages) break;
     }
-    if (a.stages >= 4 || a.rp == 1) break;
+    if (a.stages >= (a.rp == kMaxPassRows ? kWideChains : 4) || a.rp == 1) break;
   }
   // (three MMA warps where accumulators of 64 columns leave none for a fourth's)
   const bool wide = a.rp == kMaxPassRows;
-  if (a.stages > (wide ? 6 : kMaxStages)) a.stages = wide ? 6 : kMaxStages;
-  a.issuers = wide || a.stages / 3 * 3 > a.stages / 4 * 4 ? 3 : 4;
+  if (a.stages > (wide ? kWideStages : kMaxStages)) a.stages = wide ? kWideStages : kMaxStages;
+  a.issuers = wide                                      ? kWideChains
+              : a.stages / 3 * 3 > a.stages / 4 * 4 ? 3
+                                                        : 4;
   a.stages = a.stages / a.issuers * a.issuers;
   a.col_sfb = 2 * a.issuers * a.xrows;
   const long long most = (long long)(a.R) * ((N + kUnitRows - 1) / kUnitRows);
